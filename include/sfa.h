@@ -353,6 +353,117 @@ SFA_API int sfa_debug_set_wait_limit(sfa_handle* h, unsigned int spin_limit, lon
  * only. */
 SFA_API int sfa_debug_set_paths(sfa_handle* h, int decode_tile, int prefill_near);
 
+/* ---- paged key/value cache ------------------------------------------------
+ * The pages replace or enhance the attention of some layers and leave the
+ * others exact ([P1 §2.1] three layers replaced; [P2]: the enhancement is
+ * added to the engine's attention output, the add output modes above).  These
+ * calls are that exact attention over a full cache, for steps of one token, of
+ * a tree of drafted tokens, or of a chunk of a prompt:
+ *   sfa_tree_plan   ancestor masks and positions of a drafted tree
+ *   sfa_kv_append   rotated keys and values into the cache, rotated q and k out
+ *   sfa_kv_attend   softmax attention of the new tokens over the cache
+ *   sfa_kv_accept   the accepted path of a tree moved up behind the context
+ * The accepted tokens then enter the SFA state by sfa_prefill_ragged.
+ *
+ * Sequence b holds ctx_lens[b] tokens in the cache before the call and has
+ * lens[b] new ones (0 <= lens[b] <= n_max; lens NULL: n_max each), which take
+ * the slots ctx_lens[b] + i.  Slot s lives in row s % page_size of page
+ * page_table[b][s / page_size].  All int arrays are DEVICE int32, read by the
+ * kernels, so an earlier kernel on the stream may write them and a captured
+ * graph sees their current contents.  Rows past lens[b] of any input take no
+ * part in any result, and of any output keep what they held.
+ *
+ * Errors found on the device are latched for sfa_check_device_status as
+ * SFA_ERR_INVALID_ARG: a sequence with ctx_lens < 0, lens outside 0 .. n_max or
+ * more tokens than max_pages * page_size is skipped (its outputs and pages stay
+ * as they are); a page id outside 0 .. n_pages - 1 that a token needs is not
+ * written by append and accept, and reads as keys and values of zero in attend.
+ * Two sequences may share pages that no call writes; a page written for one
+ * sequence belongs to it alone. */
+typedef struct sfa_kv_cache {
+  void* k_pages;         /* DEVICE [n_layers][n_pages][n_kv][page_size][d] in_dtype       */
+  void* v_pages;         /* DEVICE, same layout                                            */
+  long long n_pages;     /* pages of a layer, n_layers * n_pages * n_kv <= 2^31 - 1        */
+  int page_size;         /* tokens of a page: 8, 16, 32, 64, 128 or 256                    */
+  int max_pages;         /* entries of a row of page_table                                 */
+  const int* page_table; /* DEVICE [batch][max_pages]; entries past a sequence's tokens are
+                            not read                                                       */
+} sfa_kv_cache;
+
+typedef enum sfa_rope_style {
+  SFA_ROPE_HALF = 0,  /* pairs (x[j], x[j + dims/2])   */
+  SFA_ROPE_PAIRS = 1  /* pairs (x[2j], x[2j + 1])      */
+} sfa_rope_style;
+
+/* Rotation of the first `dims` elements of a head: pair j of a token at
+ * position p turns by the angle p * f_j, f_j = base^(-2j/dims) or inv_freq[j].
+ * Angles are reduced in 64 bits, so that far positions keep fp32 accuracy. */
+typedef struct sfa_rope {
+  int style;              /* sfa_rope_style                                         */
+  int dims;               /* rotated elements, a multiple of 16 up to d; 0: all of d */
+  double base;            /* > 0 and finite; not used with inv_freq                  */
+  const double* inv_freq; /* HOST [dims / 2] finite values, read by the call; or NULL */
+} sfa_rope;
+
+#define SFA_TREE_MAX 1024 /* most nodes of a tree, and of the rows of a mask or path */
+
+/* Masks and positions of trees of drafted tokens.  parents [batch][n_max]:
+ * node i's parent, -1 (none) <= parents[b][i] < i.  positions [batch][n_max] =
+ * ctx_lens[b] + depth of the node (0 for a node without parent); mask
+ * [batch][n_max][(n_max + 31) / 32]: bit j % 32 of word j / 32 of row i is 1
+ * where node j is node i or one of its ancestors.  Either output may be NULL.
+ * A sequence with a parent out of range is skipped and latched as
+ * SFA_ERR_INVALID_ARG.  SFA_ERR_UNSUPPORTED for n_max > SFA_TREE_MAX. */
+SFA_API int sfa_tree_plan(const sfa_handle* h, const int* parents, int n_max, const int* lens,
+                          const int* ctx_lens, int batch, int* positions, uint32_t* mask, void* stream);
+
+/* Appends the new tokens' keys, rotated to their positions, and values to the
+ * cache, for layers layer_begin .. layer_begin + layer_count - 1.
+ * q [layer_count][batch][n_max][n_q][d], k and v [layer_count][batch][n_max]
+ * [n_kv][d] in in_dtype.  q_out and k_out, the layouts of q and k: rotated
+ * queries and keys, each may be NULL or the input itself; q may be NULL with
+ * q_out.  positions [batch][n_max] int32, or NULL for ctx_lens[b] + i.  rope
+ * (HOST): NULL for no rotation.  The rotation is computed in fp32 and rounded
+ * once to in_dtype; values are copied bit for bit.  n_max == 0 enqueues nothing. */
+SFA_API int sfa_kv_append(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begin, int layer_count,
+                          const void* q, const void* k, const void* v, int n_max, const int* lens,
+                          const int* ctx_lens, const int* positions, const sfa_rope* rope, int batch,
+                          void* q_out, void* k_out, void* stream);
+
+/* Bytes of workspace of sfa_kv_attend (partial results of sequences that are
+ * split over CTAs); 0 on invalid input.  It depends on n_max up to some
+ * rows only, never on the lengths; its content need not be initialised.  A
+ * workspace serves one call at a time: calls that may overlap on the GPU
+ * (other streams, graphs replayed side by side) each need their own. */
+SFA_API size_t sfa_kv_attend_workspace_bytes(const sfa_handle* h, int n_max);
+
+/* Exact attention of the new tokens, whose keys and values are in the cache
+ * already (sfa_kv_append): out_i[h] = sum_j p_j v_j[g], p = softmax over the
+ * visible j of <q_i[h], k_j[g]> / sqrt(d), g = h / (n_q / n_kv).  Node i sees the
+ * ctx_lens[b] cached tokens and, of the new ones, those of its row of mask (the
+ * layout of sfa_tree_plan; bits at or past lens[b] are ignored), or with mask
+ * NULL the ones up to itself.  A node that sees nothing gets zeros.  Keys and
+ * values that a node does not see have no influence on it, NaN and infinities
+ * among them.  q [layer_count][batch][n_max][n_q][d], out [layer_count][batch]
+ * [n_max][hidden], both in_dtype (out is thus the attention output that
+ * SFA_OUT_ADD_BF16 or SFA_OUT_ADD_F32 adds to).  SFA_ERR_UNSUPPORTED for a mask
+ * with n_max > SFA_TREE_MAX, layer_count * batch * n_max * n_q > 2^31 - 1.
+ * SFA_ERR_WORKSPACE if workspace is too small. */
+SFA_API int sfa_kv_attend(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begin, int layer_count,
+                          const void* q, int n_max, const int* lens, const int* ctx_lens,
+                          const uint32_t* mask, int batch, void* out, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Moves the accepted nodes' keys and values up behind the context: slot
+ * ctx_lens[b] + path[b][i] -> ctx_lens[b] + i for i < n_accept[b], in order.
+ * path [batch][n_max]: strictly increasing node indices in 0 .. n_max - 1.  A
+ * sequence with a path that is not, or n_accept outside 0 .. n_max, is skipped
+ * and latched as SFA_ERR_INVALID_ARG.  ctx_lens is not changed: the caller adds
+ * n_accept.  SFA_ERR_UNSUPPORTED for n_max > SFA_TREE_MAX. */
+SFA_API int sfa_kv_accept(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begin, int layer_count,
+                          const int* path, int n_max, const int* n_accept, const int* ctx_lens, int batch,
+                          void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -44,6 +44,10 @@ SFA_OUT_BF16 = 1      # out bf16 = x + enhancement
 SFA_OUT_ADD_F32 = 2   # out fp32 += enhancement (out holds the caller's attention output)
 SFA_OUT_ADD_BF16 = 3  # out bf16 += enhancement
 
+SFA_ROPE_HALF = 0     # rotation pairs (x[j], x[j + dims/2])
+SFA_ROPE_PAIRS = 1    # rotation pairs (x[2j], x[2j + 1])
+SFA_TREE_MAX = 1024   # most nodes of a drafted tree
+
 EXPORTED = (
     "sfa_config_default", "sfa_config_validate", "sfa_state_layout_for", "sfa_init",
     "sfa_destroy", "sfa_state_bytes", "sfa_prefill_workspace_bytes", "sfa_state_reset",
@@ -51,6 +55,8 @@ EXPORTED = (
     "sfa_abi_version", "sfa_debug_set_wait_limit", "sfa_debug_set_paths", "sfa_prefill_static_ws",
     "sfa_prefill_layers_workspace_bytes", "sfa_prefill_layers", "sfa_decode_step_ex",
     "sfa_set_decode_input_prefetch", "sfa_prefill_ragged", "sfa_set_output_mode",
+    "sfa_tree_plan", "sfa_kv_append", "sfa_kv_attend_workspace_bytes", "sfa_kv_attend",
+    "sfa_kv_accept",
 )
 
 
@@ -76,6 +82,17 @@ class sfa_state_layout(ctypes.Structure):
     _fields_ = [(name, ctypes.c_size_t) for name in (
         "header_bytes", "stream_stride", "total_bytes", "off_pos", "off_win_k", "off_win_v",
         "off_far", "off_field", "off_ring_sum", "off_ring")]
+
+
+class sfa_kv_cache(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("n_pages", ctypes.c_longlong), ("page_size", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("page_table", ctypes.c_void_p)]
+
+
+class sfa_rope(ctypes.Structure):
+    _fields_ = [("style", ctypes.c_int), ("dims", ctypes.c_int), ("base", ctypes.c_double),
+                ("inv_freq", ctypes.POINTER(ctypes.c_double))]
 
 
 _lock = threading.Lock()
@@ -119,6 +136,12 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
             "sfa_set_decode_input_prefetch": (i, [vp, i]),
             "sfa_prefill_ragged": (i, [vp, vp, vp, vp, ll, vp, i, vp, vp, vp, sz, vp]),
             "sfa_set_output_mode": (i, [vp, i]),
+            "sfa_tree_plan": (i, [vp, vp, i, vp, vp, i, vp, vp, vp]),
+            "sfa_kv_append": (i, [vp, P(sfa_kv_cache), i, i, vp, vp, vp, i, vp, vp, vp,
+                                  P(sfa_rope), i, vp, vp, vp]),
+            "sfa_kv_attend_workspace_bytes": (sz, [vp, i]),
+            "sfa_kv_attend": (i, [vp, P(sfa_kv_cache), i, i, vp, i, vp, vp, vp, i, vp, vp, sz, vp]),
+            "sfa_kv_accept": (i, [vp, P(sfa_kv_cache), i, i, vp, i, vp, vp, i, vp]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(lib, name)
@@ -571,6 +594,236 @@ class SfaOperator:
         return sfa_state_layout_for(_layout_cfg(self.cfg), self.batch)
 
 
+# ------------------------------------------------------ paged key/value cache
+
+
+class SfaRope:
+    """Position rotation of sfa_kv_append (``sfa_rope``): the first ``dims``
+    elements of a head (0: all), in ``style`` SFA_ROPE_HALF or SFA_ROPE_PAIRS,
+    pair j turning by base ** (-2j/dims) or inv_freq[j] per position."""
+
+    def __init__(self, base: float = 10000.0, style: int = SFA_ROPE_HALF, dims: int = 0,
+                 inv_freq=None):
+        self.base, self.style, self.dims = float(base), int(style), int(dims)
+        self.inv_freq = None if inv_freq is None else [float(f) for f in inv_freq]
+        if self.inv_freq is not None and self.dims and len(self.inv_freq) < self.dims // 2:
+            raise ValueError(f"inv_freq has {len(self.inv_freq)} values, needs {self.dims // 2}")
+        self._arr = (None if self.inv_freq is None
+                     else (ctypes.c_double * len(self.inv_freq))(*self.inv_freq))
+        self.c = sfa_rope(self.style, self.dims, self.base, self._arr)
+
+    def check(self, head_dim: int) -> None:
+        need = (self.dims or head_dim) // 2
+        if self.inv_freq is not None and len(self.inv_freq) < need:
+            raise ValueError(f"inv_freq has {len(self.inv_freq)} values, needs {need}")
+
+
+def _ints(t, name: str, shape, device) -> Optional[int]:
+    """Pointer of a contiguous int32 tensor of exactly `shape` on `device`."""
+    if t is None:
+        return None
+    p = _dev(t, name, torch.int32)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return p
+
+
+def _rows(t, name: str, shape, dtype, device) -> int:
+    p = _dev(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return p
+
+
+def _call_on(device, stream, fn, *args) -> int:
+    """fn(*args, stream) with `device` current; stream None is that device's
+    current stream."""
+    if device.type != "cuda" or device.index is None or device.index == torch.cuda.current_device():
+        return fn(*args, _stream_ptr(stream))
+    with torch.cuda.device(device):
+        return fn(*args, _stream_ptr(stream))
+
+
+def sfa_tree_plan(h: Handle, parents: torch.Tensor, ctx_lens: torch.Tensor,
+                  lens: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                  mask: Optional[torch.Tensor] = None, stream=None):
+    """Positions [B, n] and ancestor masks [B, n, (n + 31) // 32] (int32) of the
+    drafted trees parents [B, n] (int32, -1: no parent, else below the node's
+    own index).  Returns (positions, mask); given tensors are written in
+    place, and rows past lens keep what they held (new ones start as zero)."""
+    if not isinstance(parents, torch.Tensor) or parents.dim() != 2:
+        raise ValueError("parents must be a [batch, n] tensor")
+    B, n = parents.shape
+    dev = parents.device
+    pp = _ints(parents, "parents", (B, n), dev)
+    cp, lp = _ints(ctx_lens, "ctx_lens", (B,), dev), _ints(lens, "lens", (B,), dev)
+    words = (n + 31) // 32
+    if positions is None:
+        positions = _zeros_for((B, n), torch.int32, dev, stream)
+    if mask is None:
+        mask = _zeros_for((B, n, words), torch.int32, dev, stream)
+    rc = _call_on(dev, stream, load_library().sfa_tree_plan, h.ptr, pp, n, lp, cp, B,
+                  _ints(positions, "positions", (B, n), dev),
+                  _ints(mask, "mask", (B, n, words), dev))
+    if rc != SFA_OK:
+        raise SfaError(rc, "sfa_tree_plan")
+    return positions, mask
+
+
+def _zeros_for(shape, dtype, device, stream):
+    """A zeroed tensor that work on `stream` may use: the fill comes first and
+    the tensor is marked as used there."""
+    t = torch.zeros(shape, dtype=dtype, device=device)
+    if isinstance(stream, torch.cuda.Stream):
+        stream.wait_stream(torch.cuda.current_stream(device))
+        t.record_stream(stream)
+    return t
+
+
+def sfa_kv_attend_workspace_bytes(h: Handle, n_max: int) -> int:
+    return int(load_library().sfa_kv_attend_workspace_bytes(h.ptr, n_max))
+
+
+class SfaPagedCache:
+    """A paged key/value cache of the handle's layers: k_pages and v_pages
+    [L, n_pages, n_kv, page_size, d] in the handle's input dtype and page_table
+    [batch, max_pages] int32.  The tensors stay the caller's: a table changed in
+    place is seen by the next call.
+
+    ``append``, ``attend`` and ``accept`` are sfa_kv_append, sfa_kv_attend and
+    sfa_kv_accept for layers layer_begin .. layer_begin + q.shape[0] - 1; q is
+    [layers, B, n, n_q, d], ctx_lens and lens [B] int32 on the device.  The
+    workspace of attend belongs to the cache, one per stream; graphs that are
+    replayed side by side, and streams given as raw pointers, need a
+    ``workspace`` of their own per graph or stream."""
+
+    def __init__(self, handle: Handle, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                 page_table: torch.Tensor):
+        c = handle.cfg
+        self.handle = handle
+        if k_pages.dim() != 5 or page_table.dim() != 2:
+            raise ValueError("k_pages must be [L, n_pages, n_kv, page_size, d] and page_table [batch, max_pages]")
+        self.device = k_pages.device
+        self.n_pages, self.page_size = k_pages.shape[1], k_pages.shape[3]
+        self.batch, self.max_pages = page_table.shape
+        shape = (c.n_layers, self.n_pages, c.n_kv_heads, self.page_size, c.head_dim)
+        kp = _rows(k_pages, "k_pages", shape, c.torch_dtype, self.device)
+        vp = _rows(v_pages, "v_pages", shape, c.torch_dtype, self.device)
+        tp = _ints(page_table, "page_table", page_table.shape, self.device)
+        self.k_pages, self.v_pages, self.page_table = k_pages, v_pages, page_table
+        self.c = sfa_kv_cache(kp, vp, self.n_pages, self.page_size, self.max_pages, tp)
+        self._ws = {}
+        self._ref = ctypes.byref(self.c)
+
+    def _lens(self, ctx_lens, lens):
+        B = self.batch
+        return (_ints(ctx_lens, "ctx_lens", (B,), self.device),
+                _ints(lens, "lens", (B,), self.device))
+
+    def _workspace(self, n: int, stream) -> torch.Tensor:
+        """This stream's workspace, grown to what n new tokens need."""
+        need = sfa_kv_attend_workspace_bytes(self.handle, n)
+        key = _stream_ptr(stream) if stream is not None else _stream_ptr(torch.cuda.current_stream(self.device))
+        ws = self._ws.get(key)
+        if ws is None or ws.numel() < need:
+            if ws is not None and isinstance(stream, torch.cuda.Stream):
+                ws.record_stream(stream)
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+            if isinstance(stream, torch.cuda.Stream):
+                ws.record_stream(stream)
+            self._ws[key] = ws
+        return ws
+
+    def append(self, layer_begin: int, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+               ctx_lens: torch.Tensor, lens: Optional[torch.Tensor] = None,
+               positions: Optional[torch.Tensor] = None, rope: Optional[SfaRope] = None,
+               q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+               stream=None):
+        """Rotated keys and values of the new tokens into their pages; returns
+        (q_out, k_out), the rotated queries (a new tensor unless given; None
+        without q) and keys (None unless given)."""
+        cfg, dev, B = self.handle.cfg, self.device, self.batch
+        if k.dim() != 5:
+            raise ValueError("k must be [layers, batch, n, n_kv, d]")
+        Lc, n = k.shape[0], k.shape[2]
+        kv = (Lc, B, n, cfg.n_kv_heads, cfg.head_dim)
+        qs = (Lc, B, n, cfg.n_q_heads, cfg.head_dim)
+        cp, lp = self._lens(ctx_lens, lens)
+        kp, vp = _rows(k, "k", kv, cfg.torch_dtype, dev), _rows(v, "v", kv, cfg.torch_dtype, dev)
+        qp = qo = ko = None
+        if q is not None:
+            qp = _rows(q, "q", qs, cfg.torch_dtype, dev)
+            if q_out is None:
+                q_out = torch.empty_like(q) if lens is None else _zeros_for(qs, q.dtype, dev, stream)
+                if isinstance(stream, torch.cuda.Stream):
+                    q_out.record_stream(stream)
+            qo = _rows(q_out, "q_out", qs, cfg.torch_dtype, dev)
+        elif q_out is not None:
+            raise ValueError("q_out needs q")
+        if k_out is not None:
+            ko = _rows(k_out, "k_out", kv, cfg.torch_dtype, dev)
+        pp = _ints(positions, "positions", (B, n), dev)
+        if rope is not None:
+            rope.check(cfg.head_dim)
+        rc = _call_on(dev, stream, load_library().sfa_kv_append, self.handle.ptr, self._ref, layer_begin, Lc,
+                      qp, kp, vp, n, lp, cp, pp, None if rope is None else ctypes.byref(rope.c), B,
+                      qo, ko)
+        if rc != SFA_OK:
+            raise SfaError(rc, "sfa_kv_append")
+        return q_out, k_out
+
+    def attend(self, layer_begin: int, q: torch.Tensor, ctx_lens: torch.Tensor,
+               lens: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+               out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+        """Attention of the new tokens (appended before) over the cache:
+        out [layers, B, n, hidden] in the input dtype.  mask [B, n, words] as of
+        sfa_tree_plan, or None: every new token sees those before it.  Rows past
+        lens keep what out held (a new out is zero there)."""
+        cfg, dev, B = self.handle.cfg, self.device, self.batch
+        if q.dim() != 5:
+            raise ValueError("q must be [layers, batch, n, n_q, d]")
+        Lc, n = q.shape[0], q.shape[2]
+        qp = _rows(q, "q", (Lc, B, n, cfg.n_q_heads, cfg.head_dim), cfg.torch_dtype, dev)
+        cp, lp = self._lens(ctx_lens, lens)
+        mp = _ints(mask, "mask", (B, n, (n + 31) // 32), dev)
+        if out is None:
+            out = _zeros_for((Lc, B, n, cfg.hidden), cfg.torch_dtype, dev, stream)
+        op = _rows(out, "out", (Lc, B, n, cfg.hidden), cfg.torch_dtype, dev)
+        if n == 0:
+            return out
+        ws = self._workspace(n, stream) if workspace is None else workspace
+        wp = _dev(ws, "workspace", torch.uint8)
+        if ws.device != dev:
+            raise ValueError(f"workspace is on {ws.device}, not on {dev}")
+        rc = _call_on(dev, stream, load_library().sfa_kv_attend, self.handle.ptr, self._ref, layer_begin, Lc,
+                      qp, n, lp, cp, mp, B, op, wp, ws.numel())
+        if rc != SFA_OK:
+            raise SfaError(rc, "sfa_kv_attend")
+        return out
+
+    def accept(self, layer_begin: int, layer_count: int, path: torch.Tensor, n_accept: torch.Tensor,
+               ctx_lens: torch.Tensor, stream=None) -> None:
+        """The keys and values of nodes path[b, :n_accept[b]] ([B, n] and [B]
+        int32, rising node indices) moved up behind the context; the caller
+        then adds n_accept to ctx_lens."""
+        if path.dim() != 2:
+            raise ValueError("path must be [batch, n]")
+        B, n = self.batch, path.shape[1]
+        pp = _ints(path, "path", (B, n), self.device)
+        cp, np_ = self._lens(ctx_lens, n_accept)
+        if np_ is None:
+            raise ValueError("n_accept must be a CUDA tensor")
+        rc = _call_on(self.device, stream, load_library().sfa_kv_accept, self.handle.ptr, self._ref, layer_begin,
+                      layer_count, pp, n, np_, cp, B)
+        if rc != SFA_OK:
+            raise SfaError(rc, "sfa_kv_accept")
+
+
 def _layout_cfg(cfg: SfaConfig) -> sfa_config:
     # Layout arithmetic needs a non-null, aligned slots pointer only for the
     # validity check; 16 is a stand-in address that is never dereferenced.
@@ -603,3 +856,9 @@ def read_state(op: SfaOperator) -> dict:
         "ring_sum": grab(lay.off_ring_sum, H * 4, torch.float32, (H,)),
         "ring": grab(lay.off_ring, 16 * H * 4, torch.float32, (16, H)),
     }
+
+
+# The C names, on a cache: sfa_kv_append(cache, layer_begin, q, k, v, ...) and so on.
+sfa_kv_append = SfaPagedCache.append
+sfa_kv_attend = SfaPagedCache.attend
+sfa_kv_accept = SfaPagedCache.accept

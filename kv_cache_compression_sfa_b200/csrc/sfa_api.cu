@@ -226,6 +226,60 @@ int prefill_impl(const sfa_handle* h, int layer_begin, int layer_count, const vo
                  const void* v, long long n, const int* lens, int batch, void* state, void* out,
                  void* workspace, size_t workspace_bytes, void* stream);
 
+// ---- paged key/value cache: checks shared by its calls
+
+constexpr int kMaxPageSize = 256;
+
+// The current device must be the handle's: its kernels' attributes, error word
+// and SM count belong there.
+bool on_device(const sfa_handle* h) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
+}
+
+int paged_status(const sfa_handle* h, int n_max, const int* ctx_lens, int batch) {
+  if (!handle_ok(h) || n_max < 0 || batch <= 0 || !ctx_lens) return SFA_ERR_INVALID_ARG;
+  return SFA_OK;
+}
+
+// Checks a cache and a layer range and fills the part of the parameters that
+// every paged call shares.
+int fill_paged(PagedParams& c, const sfa_handle* h, const sfa_kv_cache* cache, int layer_begin, int layer_count,
+               int n_max, const int* lens, const int* ctx_lens, int batch) {
+  if (!cache || !cache->k_pages || !cache->v_pages || !cache->page_table) return SFA_ERR_INVALID_ARG;
+  if (layer_begin < 0 || layer_count <= 0 || layer_count > h->cfg.n_layers ||
+      layer_begin > h->cfg.n_layers - layer_count)
+    return SFA_ERR_INVALID_ARG;
+  const int ps = cache->page_size;
+  if (ps <= 0 || cache->n_pages <= 0 || cache->max_pages <= 0) return SFA_ERR_INVALID_ARG;
+  if (!aligned16(cache->k_pages) || !aligned16(cache->v_pages)) return SFA_ERR_ALIGNMENT;
+  if (ps < 8 || ps > kMaxPageSize || (ps & (ps - 1)) != 0) return SFA_ERR_UNSUPPORTED;
+  if (cache->n_pages > 0x7fffffffLL ||
+      cache->n_pages * h->cfg.n_layers > 0x7fffffffLL / h->cfg.n_kv_heads ||
+      static_cast<long long>(cache->max_pages) * ps > 0x7fffffffLL)
+    return SFA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(layer_count) * batch > 0x7fffffffLL) return SFA_ERR_UNSUPPORTED;
+  c.k_pages = cache->k_pages;
+  c.v_pages = cache->v_pages;
+  c.table = cache->page_table;
+  c.n_pages = cache->n_pages;
+  c.ps = ps;
+  c.ps_log2 = 0;
+  while ((1 << c.ps_log2) < ps) ++c.ps_log2;
+  c.max_pages = cache->max_pages;
+  c.l0 = layer_begin;
+  c.Lc = layer_count;
+  c.B = batch;
+  c.n_max = n_max;
+  c.nq = h->cfg.n_q_heads;
+  c.nkv = h->cfg.n_kv_heads;
+  c.G = c.nq / c.nkv;
+  c.lens = lens;
+  c.ctx = ctx_lens;
+  c.err = h->err;
+  return SFA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -322,6 +376,7 @@ int sfa_init(const sfa_config* cfg, sfa_handle** out) {
   if (e == cudaSuccess) e = prefill_prepare(h->device);
   if (e == cudaSuccess) e = decode_prepare(h->device);
   if (e == cudaSuccess) e = decode_tile_prepare(h->device);
+  if (e == cudaSuccess) e = attend_prepare(h->device);
   if (e == cudaSuccess) {
     // Prefill near-field plan; the decode kernels' cluster size: the first
     // candidate whose decode plan fits and of which one cluster fits on the
@@ -673,6 +728,123 @@ int sfa_debug_set_paths(sfa_handle* h, int decode_tile, int prefill_near) {
   }
   h->tile_mode = decode_tile;
   return SFA_OK;
+}
+
+int sfa_tree_plan(const sfa_handle* h, const int* parents, int n_max, const int* lens, const int* ctx_lens,
+                  int batch, int* positions, uint32_t* mask, void* stream) {
+  const int st = paged_status(h, n_max, ctx_lens, batch);
+  if (st != SFA_OK) return st;
+  if (!parents || (!positions && !mask)) return SFA_ERR_INVALID_ARG;
+  if (n_max > SFA_TREE_MAX) return SFA_ERR_UNSUPPORTED;
+  if (n_max == 0) return SFA_OK;
+  if (!on_device(h)) return SFA_ERR_INVALID_ARG;
+  PlanParams p;
+  p.parents = parents;
+  p.lens = lens;
+  p.ctx = ctx_lens;
+  p.positions = positions;
+  p.mask = mask;
+  p.n_max = n_max;
+  p.words = (n_max + 31) / 32;
+  p.B = batch;
+  p.err = h->err;
+  return cuda_status(launch_tree_plan(p, static_cast<cudaStream_t>(stream)));
+}
+
+int sfa_kv_append(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begin, int layer_count, const void* q,
+                  const void* k, const void* v, int n_max, const int* lens, const int* ctx_lens,
+                  const int* positions, const sfa_rope* rope, int batch, void* q_out, void* k_out, void* stream) {
+  int st = paged_status(h, n_max, ctx_lens, batch);
+  if (st != SFA_OK) return st;
+  AppendParams p;
+  std::memset(&p, 0, sizeof(p));
+  st = fill_paged(p.c, h, cache, layer_begin, layer_count, n_max, lens, ctx_lens, batch);
+  if (st != SFA_OK) return st;
+  if (!k || !v || (q == nullptr) != (q_out == nullptr)) return SFA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out))
+    return SFA_ERR_ALIGNMENT;
+  if (rope) {
+    const int d = h->cfg.head_dim, dims = rope->dims == 0 ? d : rope->dims;
+    if (rope->style != SFA_ROPE_HALF && rope->style != SFA_ROPE_PAIRS) return SFA_ERR_INVALID_ARG;
+    if (dims < 0 || dims > d || dims % 16 != 0) return SFA_ERR_INVALID_ARG;
+    if (!rope->inv_freq && !(std::isfinite(rope->base) && rope->base > 0.0)) return SFA_ERR_INVALID_ARG;
+    const double two_pi = 6.283185307179586476925286766559;
+    for (int j = 0; j < dims / 2; ++j) {
+      const double f = rope->inv_freq ? rope->inv_freq[j] : std::pow(rope->base, -2.0 * j / dims);
+      if (!std::isfinite(f)) return SFA_ERR_INVALID_ARG;
+      p.turns[j] = f / two_pi;
+    }
+    p.style = rope->style;
+    p.dims = dims;
+  }
+  if (n_max == 0) return SFA_OK;
+  if (!on_device(h)) return SFA_ERR_INVALID_ARG;
+  if (static_cast<long long>(layer_count) * batch > 0x7fffffffLL / n_max) return SFA_ERR_UNSUPPORTED;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.positions = positions;
+  return cuda_status(launch_kv_append(p, h->cfg.in_dtype, h->cfg.head_dim, h->n_sm, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sfa_kv_attend_workspace_bytes(const sfa_handle* h, int n_max) {
+  if (!handle_ok(h) || n_max <= 0) return 0;
+  const sfa_config* c = &h->cfg;
+  return attend_plan(c->in_dtype, c->head_dim, c->n_q_heads / c->n_kv_heads, n_max, h->n_sm).total;
+}
+
+int sfa_kv_attend(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begin, int layer_count, const void* q,
+                  int n_max, const int* lens, const int* ctx_lens, const uint32_t* mask, int batch, void* out,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  int st = paged_status(h, n_max, ctx_lens, batch);
+  if (st != SFA_OK) return st;
+  AttendParams p;
+  std::memset(&p, 0, sizeof(p));
+  st = fill_paged(p.c, h, cache, layer_begin, layer_count, n_max, lens, ctx_lens, batch);
+  if (st != SFA_OK) return st;
+  if (n_max == 0) return SFA_OK;
+  if (!q || !out) return SFA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return SFA_ERR_ALIGNMENT;
+  const sfa_config* c = &h->cfg;
+  if ((mask && n_max > SFA_TREE_MAX) || batch > kAttendMaxBatch ||
+      static_cast<long long>(layer_count) * batch * c->n_q_heads > 0x7fffffffLL / n_max)
+    return SFA_ERR_UNSUPPORTED;
+  const AttendPlan a = attend_plan(c->in_dtype, c->head_dim, p.c.G, n_max, h->n_sm);
+  if (!workspace || workspace_bytes < a.total) return SFA_ERR_WORKSPACE;
+  if (!on_device(h)) return SFA_ERR_INVALID_ARG;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  p.q = q;
+  p.out = out;
+  p.mask = mask;
+  p.words = (n_max + 31) / 32;
+  p.rows_step = a.rows_step;
+  p.kt = a.kt;
+  p.n_cta = a.n_cta;
+  p.min_tiles = 1;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(c->head_dim)));
+  p.meta = reinterpret_cast<SplitMeta*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + a.off_ml);
+  p.part_o = reinterpret_cast<float*>(ws + a.off_o);
+  return cuda_status(launch_kv_attend(p, c->in_dtype, c->head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+int sfa_kv_accept(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begin, int layer_count, const int* path,
+                  int n_max, const int* n_accept, const int* ctx_lens, int batch, void* stream) {
+  int st = paged_status(h, n_max, ctx_lens, batch);
+  if (st != SFA_OK) return st;
+  AcceptParams p;
+  std::memset(&p, 0, sizeof(p));
+  st = fill_paged(p.c, h, cache, layer_begin, layer_count, n_max, nullptr, ctx_lens, batch);
+  if (st != SFA_OK) return st;
+  if (!path || !n_accept) return SFA_ERR_INVALID_ARG;
+  if (n_max > SFA_TREE_MAX) return SFA_ERR_UNSUPPORTED;
+  if (n_max == 0) return SFA_OK;
+  if (!on_device(h)) return SFA_ERR_INVALID_ARG;
+  p.path = path;
+  p.n_accept = n_accept;
+  return cuda_status(launch_kv_accept(p, h->cfg.in_dtype, h->cfg.head_dim, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

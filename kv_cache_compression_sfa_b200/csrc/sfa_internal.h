@@ -194,4 +194,90 @@ cudaError_t launch_slot_norms(const float* slots, float* norms, int L, int H, cu
 // 64 x 64 blocks, 8 KB each); H must be a multiple of 64.
 cudaError_t launch_slot_image(const float* slots, unsigned char* img, int L, int H, cudaStream_t s);
 
+// ---- paged key/value cache -------------------------------------------------
+
+// What every paged call knows of its cache and batch.
+struct PagedParams {
+  void* k_pages;            // [L][n_pages][nkv][ps][D]
+  void* v_pages;
+  const int* table;         // [B][max_pages]
+  long long n_pages;
+  int ps, ps_log2, max_pages;
+  int l0, Lc, B, n_max, nq, nkv, G;
+  const int* lens;          // [B] new tokens, or null: n_max each
+  const int* ctx;           // [B] tokens cached before the call
+  int* err;
+};
+
+constexpr int kMaxRopePairs = 64;  // head_dim / 2
+struct AppendParams {
+  PagedParams c;
+  const void* q;            // may be null
+  const void* k;
+  const void* v;
+  void* q_out;              // may be null, or q
+  void* k_out;              // may be null, or k
+  const int* positions;     // [B][n_max], or null: ctx + i
+  int style, dims;          // sfa_rope; dims = 0: no rotation
+  int tokens_per_cta;
+  double turns[kMaxRopePairs];  // f_j / (2 pi): turns per position
+};
+
+struct AcceptParams {
+  PagedParams c;            // n_max: row length of path
+  const int* path;
+  const int* n_accept;
+};
+
+struct PlanParams {
+  const int* parents;
+  const int* lens;
+  const int* ctx;
+  int* positions;
+  uint32_t* mask;
+  int n_max, words, B;
+  int* err;
+};
+
+// A partial result of an attend call that is split over CTAs: written by the
+// CTA that starts the split item, read by the combine kernel.
+struct SplitMeta {
+  int last_cta;             // CTA of the item's last piece; -1: this CTA starts no split item
+  int l, b, kh;             // the item
+  int row0, rows;           // its first row (node * G + head of the group) and row count
+  int pad[2];
+};
+
+struct AttendParams {
+  PagedParams c;
+  const void* q;
+  void* out;
+  const uint32_t* mask;     // [B][n_max][words], or null: causal
+  int words;
+  int rows_step;            // rows (node * G + head) of a work item
+  int kt;                   // keys of a tile
+  int n_cta;                // CTAs that share the tiles
+  int min_tiles;            // fewest tiles of a CTA
+  float scale_log2;         // log2(e) / sqrt(d)
+  SplitMeta* meta;          // [n_cta]
+  float* part_ml;           // [n_cta][2][rows_step][2]: running maximum (log2 units), sum
+  float* part_o;            // [n_cta][2][rows_step][D], unnormalised
+};
+
+constexpr int kAttendMaxBatch = 4096;  // sequences of an attend call (prefix sums in shared memory)
+
+// Rows of a work item and keys of a tile of the attend kernels, and the
+// workspace that they need.
+struct AttendPlan {
+  int rows_step, kt, n_cta;
+  size_t off_ml, off_o, total;
+};
+AttendPlan attend_plan(int in_dtype, int head_dim, int G, int n_max, int n_sm);
+
+cudaError_t launch_tree_plan(const PlanParams& p, cudaStream_t s);
+cudaError_t launch_kv_append(const AppendParams& p, int in_dtype, int head_dim, int n_sm, cudaStream_t s);
+cudaError_t launch_kv_accept(const AcceptParams& p, int in_dtype, int head_dim, cudaStream_t s);
+cudaError_t launch_kv_attend(const AttendParams& p, int in_dtype, int head_dim, cudaStream_t s);
+cudaError_t attend_prepare(int device);
+
 }  // namespace sfa
