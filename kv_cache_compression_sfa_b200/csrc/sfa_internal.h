@@ -279,5 +279,8 @@ cudaError_t launch_kv_append(const AppendParams& p, int in_dtype, int head_dim, 
 cudaError_t launch_kv_accept(const AcceptParams& p, int in_dtype, int head_dim, cudaStream_t s);
 cudaError_t launch_kv_attend(const AttendParams& p, int in_dtype, int head_dim, cudaStream_t s);
 cudaError_t attend_prepare(int device);
+void attend_tc_rows(int G, int n_max, int* rows_step, int* kt);
+cudaError_t attend_tc_prepare();
+cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, cudaStream_t s);
 
 }  // namespace sfa

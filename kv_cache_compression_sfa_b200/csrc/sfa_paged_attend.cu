@@ -65,7 +65,7 @@ __device__ __forceinline__ void simt_load(const AttendParams& p, const AttendIte
 // shared-memory cycles as FMA cycles; few rows take a small RPW and are bound by
 // the cache's bytes.
 template <typename T, int D, int RPW>
-__global__ void __launch_bounds__(kSimtThreads) attend_simt_kernel(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(kSimtThreads, 1) attend_simt_kernel(const __grid_constant__ AttendParams p) {
   using P = SimtPlan<T, D, RPW>;
   constexpr int DPL = D / 32;  // output elements of a lane
   extern __shared__ __align__(16) unsigned char smem[];
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt_kernel(const __grid_
         const int row = it.row0 + rr, node = row / p.c.G, g = row - node * p.c.G;
         T* dst = static_cast<T*>(p.out) + (((static_cast<long long>(it.l) * p.c.B + it.b) * p.c.n_max + node) * p.c.nq +
                                            it.kh * p.c.G + g) * D + lane * DPL;
-        const float inv = m[r] == -INFINITY ? 0.f : 1.0f / sum;
+        const float inv = sum == 0.f ? 0.f : 1.0f / sum;  // a row that sees nothing is zero
 #pragma unroll
         for (int e = 0; e < DPL; ++e) dst[e] = static_cast<T>(o[r][e] * inv);
       } else {
@@ -233,12 +233,12 @@ __global__ void __launch_bounds__(256) attend_combine_kernel(const __grid_consta
     const float w = exp2_approx(ml.x - base);
     float v[DPL];
     VecLoad<float, DPL>::run(p.part_o + a * D + lane * DPL, v);
-    const bool some = ml.x != -INFINITY;  // a piece without visible keys holds nothing
+    const bool some = ml.y != 0.f;  // a piece without visible keys holds nothing
     sum = some ? fmaf(ml.y, w, sum) : sum;
 #pragma unroll
     for (int e = 0; e < DPL; ++e) o[e] = some ? fmaf(v[e], w, o[e]) : o[e];
   }
-  const float inv = mx == -INFINITY ? 0.f : 1.0f / sum;
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
   const int row = m.row0 + r, node = row / p.c.G, g = row - node * p.c.G;
   T* dst = static_cast<T*>(p.out) + (((static_cast<long long>(m.l) * p.c.B + m.b) * p.c.n_max + node) * p.c.nq +
                                      m.kh * p.c.G + g) * D + lane * DPL;
@@ -269,32 +269,34 @@ cudaError_t launch_simt(const AttendParams& p, cudaStream_t s) {
                     SimtPlan<T, D, RPW>::total, p, s);
 }
 
-template <typename T, int D>
-cudaError_t launch_attend_t(const AttendParams& p, cudaStream_t s) {
-  cudaError_t e;
+template <int D>
+cudaError_t launch_simt_rows(const AttendParams& p, cudaStream_t s) {
   switch (p.rows_step / kSimtWarps) {
-    case 1: e = launch_simt<T, D, 1>(p, s); break;
-    case 2: e = launch_simt<T, D, 2>(p, s); break;
-    case 4: e = launch_simt<T, D, 4>(p, s); break;
-    default: e = launch_simt<T, D, 8>(p, s); break;
+    case 1: return launch_simt<float, D, 1>(p, s);
+    case 2: return launch_simt<float, D, 2>(p, s);
+    case 4: return launch_simt<float, D, 4>(p, s);
+    default: return launch_simt<float, D, 8>(p, s);
   }
-  if (e != cudaSuccess) return e;
+}
+
+template <typename T, int D>
+cudaError_t launch_combine(const AttendParams& p, cudaStream_t s) {
   const long long rows = std::min<long long>(p.rows_step, static_cast<long long>(p.c.n_max) * p.c.G);
   return launch_pdl(attend_combine_kernel<T, D>,
                     dim3(static_cast<unsigned>(p.n_cta), static_cast<unsigned>((rows + 7) / 8), 1), 256, 0, p, s);
 }
 
-template <typename T, int D, int RPW>
+template <int D, int RPW>
 cudaError_t allow() {
-  return cudaFuncSetAttribute(attend_simt_kernel<T, D, RPW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              SimtPlan<T, D, RPW>::total);
+  return cudaFuncSetAttribute(attend_simt_kernel<float, D, RPW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              SimtPlan<float, D, RPW>::total);
 }
-template <typename T, int D>
+template <int D>
 cudaError_t allow_all() {
-  cudaError_t e = allow<T, D, 1>();
-  if (e == cudaSuccess) e = allow<T, D, 2>();
-  if (e == cudaSuccess) e = allow<T, D, 4>();
-  if (e == cudaSuccess) e = allow<T, D, 8>();
+  cudaError_t e = allow<D, 1>();
+  if (e == cudaSuccess) e = allow<D, 2>();
+  if (e == cudaSuccess) e = allow<D, 4>();
+  if (e == cudaSuccess) e = allow<D, 8>();
   return e;
 }
 
@@ -302,30 +304,36 @@ cudaError_t allow_all() {
 
 AttendPlan attend_plan(int in_dtype, int head_dim, int G, int n_max, int n_sm) {
   AttendPlan a;
-  const long long rows = static_cast<long long>(n_max) * G;
-  a.kt = kSimtKeys;
-  a.rows_step = kSimtWarps * simt_rpw(static_cast<int>(std::min<long long>(rows, 64)));
+  if (in_dtype == SFA_F32) {
+    a.kt = kSimtKeys;
+    a.rows_step = kSimtWarps * simt_rpw(static_cast<int>(std::min<long long>(static_cast<long long>(n_max) * G, 64)));
+  } else {
+    attend_tc_rows(G, n_max, &a.rows_step, &a.kt);
+  }
   a.n_cta = n_sm;
   a.off_ml = static_cast<size_t>(align256(static_cast<long long>(sizeof(SplitMeta)) * a.n_cta));
   a.off_o = a.off_ml + static_cast<size_t>(align256(16LL * a.n_cta * a.rows_step));
   a.total = a.off_o + static_cast<size_t>(align256(8LL * a.n_cta * a.rows_step * head_dim));
-  (void)in_dtype;
   return a;
 }
 
 cudaError_t attend_prepare(int device) {
   (void)device;
-  cudaError_t e = allow_all<float, 64>();
-  if (e == cudaSuccess) e = allow_all<float, 128>();
-  if (e == cudaSuccess) e = allow_all<__nv_bfloat16, 64>();
-  if (e == cudaSuccess) e = allow_all<__nv_bfloat16, 128>();
+  cudaError_t e = allow_all<64>();
+  if (e == cudaSuccess) e = allow_all<128>();
+  if (e == cudaSuccess) e = attend_tc_prepare();
   return e;
 }
 
 cudaError_t launch_kv_attend(const AttendParams& p, int in_dtype, int head_dim, cudaStream_t s) {
+  cudaError_t e;
   if (in_dtype == SFA_F32)
-    return head_dim == 64 ? launch_attend_t<float, 64>(p, s) : launch_attend_t<float, 128>(p, s);
-  return head_dim == 64 ? launch_attend_t<__nv_bfloat16, 64>(p, s) : launch_attend_t<__nv_bfloat16, 128>(p, s);
+    e = head_dim == 64 ? launch_simt_rows<64>(p, s) : launch_simt_rows<128>(p, s);
+  else
+    e = launch_attend_tc(p, head_dim, s);
+  if (e != cudaSuccess) return e;
+  if (in_dtype == SFA_F32) return head_dim == 64 ? launch_combine<float, 64>(p, s) : launch_combine<float, 128>(p, s);
+  return head_dim == 64 ? launch_combine<__nv_bfloat16, 64>(p, s) : launch_combine<__nv_bfloat16, 128>(p, s);
 }
 
 }  // namespace sfa

@@ -1,0 +1,748 @@
+// sfa_paged_attend_tc.cu — attention of new tokens over the paged cache on the
+// 5th-generation tensor cores (bf16).
+//
+// A CTA walks its run of key tiles (sfa_paged.cuh) with ten warps:
+//   warp 8     loads: q by one tensor copy per 64 columns, keys and values
+//              page by page into a ring of 128-key buffers;
+//   warp 9     issues the products: S = Q K^T (both operands in shared memory,
+//              K-major), O += P V (P in tensor memory, V MN-major);
+//   warps 0-3  the softmax of stream 0, a thread per row;
+//   warps 4-7  the softmax of stream 1.
+// The two streams keep the tensor cores busy while one of them computes its
+// softmax.  With more rows than one 128-row tile (PAIR) they are two row tiles
+// that share every key and value tile; with fewer they take the key tiles of
+// one row tile in turn, each with its own maximum, sum and output, which are
+// joined in tensor memory at the end.  P overwrites the scores it came from.
+// Rows are (node, query head of the group), so that one KV head's tile serves
+// all of its query heads.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "sfa_paged.cuh"
+#include "sfa_umma.cuh"
+
+namespace sfa {
+namespace {
+
+constexpr int kTcThreads = 320;
+constexpr int kTcLoadWarp = 8;
+constexpr int kTcMmaWarp = 9;
+constexpr int kTcKeys = 128;     // keys of a tile
+constexpr int kTcRows = 128;     // rows of a row tile (tensor-memory lanes)
+constexpr uint32_t kTmemCols = 512;
+constexpr unsigned kTcPollLimit = 1u << 22;  // polls of a bounded wait
+constexpr float kRescaleLog2 = 8.0f;  // the maximum moves only when it grows by more than this (log2)
+
+// Shared memory: q (one row tile, or two), then the ring; all blocks
+// [64 columns][128 rows][128 bytes], 128-byte swizzled.
+template <int D, bool PAIR>
+struct TcPlan {
+  static constexpr int tile = kTcKeys * D * 2;          // a key, value or q tile
+  static constexpr int q = 0;
+  static constexpr int ring = (PAIR ? 2 : 1) * tile;
+  static constexpr int stages = D == 128 ? (PAIR ? 5 : 6) : (PAIR ? 11 : 12);
+  static constexpr int shared = ring + stages * tile;   // TcShared
+};
+
+struct TcMaps {
+  CUtensorMap q, k, v;
+};
+
+struct TcBars {
+  uint64_t q_full, q_empty;
+  uint64_t kv_full[12], kv_empty[12];
+  uint64_t s_full[2], p_full[2], o_done[2], drain;
+};
+
+struct TcShared {
+  AttendRun run;
+  TcBars bars;
+  float2 ml[2][kTcRows];  // maximum and sum of both streams' rows
+  int bad[2];             // clean_values found elements that are not finite
+  uint32_t tmem;
+};
+
+// Shared-memory matrix descriptor with 128-byte swizzle.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, unsigned lbo, unsigned sbo) {
+  uint64_t d = static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]; issued by one thread.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc,
+                                             bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(tmem_d), "r"(tmem_a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+
+// 32 columns of this thread's lane, without waiting: tmem_ld_wait() before use.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+        "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
+        "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
+        "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr));
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));  // no use before the wait
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+      ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+      "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
+      "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]),
+      "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+      ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+      "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Pieces of a run, the same walk in every role.
+struct PieceWalk {
+  AttendItem it;
+  int t0, t1;
+  long long left;
+  __device__ __forceinline__ explicit PieceWalk(const AttendRun& r) : it(r.it), t0(r.tile), t1(0), left(r.tiles) {
+    if (left > 0) t1 = static_cast<int>(min(static_cast<long long>(it.nt), t0 + left));
+  }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ void next(const AttendParams& p) {
+    left -= t1 - t0;
+    if (left <= 0) return;
+    next_item(p, it);
+    t0 = 0;
+    t1 = static_cast<int>(min(static_cast<long long>(it.nt), left));
+  }
+};
+
+// Bit i: key col0 + i is visible to `node`.
+__device__ __forceinline__ uint32_t visible_bits(const AttendParams& p, const AttendItem& it, int node, int col0) {
+  auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };
+  if (!p.mask) return below(it.ctx + min(node + 1, it.len) - col0);
+  const int rel0 = col0 - it.ctx;
+  if (rel0 <= -32) return 0xffffffffu;
+  const uint32_t* m = p.mask + (static_cast<long long>(it.b) * p.c.n_max + node) * p.words;
+  uint32_t bits;
+  if (rel0 < 0) {
+    bits = (m[0] << (-rel0)) | below(-rel0);
+  } else {
+    const int w = rel0 >> 5, sh = rel0 & 31;
+    const uint32_t lo = w < p.words ? m[w] : 0u;
+    const uint32_t hi = w + 1 < p.words ? m[w + 1] : 0u;
+    bits = __funnelshift_r(lo, hi, sh);
+  }
+  return bits & below(it.ctx + it.len - col0);
+}
+
+// The masked tiles' values: rows past the item's keys become zero, and
+// elements that are not finite too (a product with a zero weight would be NaN
+// in rows that do not see them); *bad is set if there were any.
+template <int D>
+__device__ __forceinline__ void clean_values(unsigned char* v, int rows, int r, int* bad) {
+  bool any = false;
+#pragma unroll
+  for (int h = 0; h < D / 64; ++h) {
+    uint4* row = reinterpret_cast<uint4*>(v + h * (kTcKeys * 128) + r * 128);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      uint4* at = row + ((c + r) & 7);
+      if (r >= rows) {
+        *at = make_uint4(0u, 0u, 0u, 0u);
+        continue;
+      }
+      uint4 x = *at;
+      uint32_t* w = &x.x;
+      bool hit = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if ((w[i] & 0x7f80u) == 0x7f80u) { w[i] &= 0xffff0000u; hit = true; }
+        if ((w[i] & 0x7f800000u) == 0x7f800000u) { w[i] &= 0x0000ffffu; hit = true; }
+      }
+      if (hit) {
+        *at = x;
+        any = true;
+      }
+    }
+  }
+  if (any) *bad = 1;
+  fence_proxy_async_smem();
+}
+
+// Elements that clean_values took out of slots slot0 .. slot1 - 1, for the rows
+// that do see them: an infinity or NaN times a positive weight.
+template <int N>
+__device__ __forceinline__ void add_nonfinite(const AttendParams& p, const AttendItem& it, int node, int slot0, int slot1,
+                                           int head_dim, int col, float* o) {
+#pragma unroll 1
+  for (int slot = slot0; slot < slot1; ++slot) {
+    if (slot >= it.ctx && !sees_new(p, it.b, node, it.len, slot - it.ctx)) continue;
+    const int pg = page_of(p.c, it.b, slot);
+    if (pg < 0) continue;
+    const long long base = ((static_cast<long long>(p.c.l0 + it.l) * p.c.n_pages + pg) * p.c.nkv + it.kh) * p.c.ps;
+    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.c.v_pages) + (base + (slot & (p.c.ps - 1))) * head_dim + col;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float x = __bfloat162float(v[e]);
+      o[e] += isfinite(x) ? 0.f : x;
+    }
+  }
+}
+
+template <int D, bool PAIR>
+__global__ void __launch_bounds__(kTcThreads, 1)
+attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ TcMaps maps) {
+  using P = TcPlan<D, PAIR>;
+  constexpr int NS = P::stages;
+  // the kernel has no other shared memory: the dynamic block starts on the 1024
+  // bytes that the swizzled tiles need
+  extern __shared__ __align__(1024) unsigned char smem[];
+  TcShared& sh = *reinterpret_cast<TcShared*>(smem + P::shared);
+  TcBars& bars = sh.bars;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    mbar_init(&bars.q_full, 1);
+    mbar_init(&bars.q_empty, 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&bars.kv_full[i], 1);
+      mbar_init(&bars.kv_empty[i], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars.s_full[s], 1);
+      mbar_init(&bars.p_full[s], 4);
+      mbar_init(&bars.o_done[s], 1);
+      sh.bad[s] = 0;
+    }
+    mbar_init(&bars.drain, 1);
+    mbar_fence_init();
+  }
+  if (warp == kTcMmaWarp) tmem_alloc(&sh.tmem, kTmemCols);
+  pdl_trigger();
+  pdl_wait();
+  find_run<kTcThreads>(p, reinterpret_cast<long long*>(smem), &sh.run);
+  fence_proxy_async_smem();  // the scratch of find_run lies where the copies land
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const AttendRun run = sh.run;
+  const uint32_t tmem = sh.tmem;
+  const int tile_rows = PAIR ? p.rows_step / 2 : p.rows_step;  // rows of one row tile
+  bool ok = true;
+
+  if (warp == kTcLoadWarp) {
+    // ---- loads.  Buffer order is the order of use: PAIR K0 V0 K1 V1 ..,
+    // else K0 K1 V0 K2 V1 ..  A lane copies one page's share of one 64-column
+    // block; page ids are read one tile ahead.
+    const int prow = min(p.c.ps, kTcKeys);                  // rows of a box
+    const int ppt = kTcKeys / prow;                          // pages of a tile
+    const int boxes = ppt * (D / 64);
+    const int my_page = lane % ppt, my_half = lane / ppt;
+    const unsigned box_off = static_cast<unsigned>(my_half * (kTcKeys * 128) + my_page * prow * 128);
+    const int z_none = static_cast<int>(static_cast<long long>(p.c.nkv) * p.c.n_pages * (p.c.l0 + p.c.Lc));
+    long long n_kv = 0;   // buffers filled so far
+    int n_q = 0;
+    for (PieceWalk w(run); w.more() && ok; w.next(p)) {
+      if (n_q > 0) ok = mbar_wait_bounded(&bars.q_empty, static_cast<unsigned>((n_q - 1) & 1), kTcPollLimit, p.c.err);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int node0 = w.it.row0 / p.c.G;
+      const int nb = tile_rows / p.c.G;
+      if (lane == 0) {
+        const unsigned qbytes = static_cast<unsigned>(tile_rows * 128 * (D / 64) * (PAIR ? 2 : 1));
+        mbar_arrive_expect_tx(&bars.q_full, qbytes);
+        for (int s = 0; s < (PAIR ? 2 : 1); ++s)
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_4d(smem + P::q + s * P::tile + h * (kTcRows * 128), &maps.q, h * 64, w.it.kh * p.c.G,
+                        node0 + s * nb, w.it.l * p.c.B + w.it.b, &bars.q_full);
+      }
+      ++n_q;
+      const int* table = p.c.table + static_cast<long long>(w.it.b) * p.c.max_pages;
+      const int slot_end = w.it.kv_end;
+      // z coordinate (page and head) of this lane's box in tile t; a box without a key reads as zeros
+      auto coord = [&](int t) -> int {
+        const int slot = t * kTcKeys + my_page * prow;
+        if (lane >= boxes || t >= w.t1 || slot >= slot_end) return z_none;
+        const int pg = table[slot >> p.c.ps_log2];
+        if (pg < 0 || pg >= p.c.n_pages) {
+          latch_error(p.c.err, SFA_ERR_INVALID_ARG);
+          return z_none;
+        }
+        return static_cast<int>((static_cast<long long>(p.c.l0 + w.it.l) * p.c.n_pages + pg) * p.c.nkv + w.it.kh);
+      };
+      auto fill = [&](const CUtensorMap* map, int t, int z) {
+        const int st = static_cast<int>(n_kv % NS);
+        if (n_kv >= NS)
+          ok = ok && mbar_wait_bounded(&bars.kv_empty[st], static_cast<unsigned>((n_kv / NS - 1) & 1), kTcPollLimit, p.c.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        if (lane == 0) mbar_arrive_expect_tx(&bars.kv_full[st], P::tile);
+        __syncwarp();
+        if (lane < boxes)
+          tma_load_3d(smem + P::ring + st * P::tile + box_off, map, my_half * 64, (t * kTcKeys) & (p.c.ps - 1) & ~(prow - 1), z,
+                      &bars.kv_full[st]);
+        ++n_kv;
+      };
+      const int n = w.t1 - w.t0;
+      if (PAIR) {
+        int z = coord(w.t0);
+        for (int i = 0; i < n && ok; ++i) {
+          const int zn = coord(w.t0 + i + 1);
+          fill(&maps.k, w.t0 + i, z);
+          if (ok) fill(&maps.v, w.t0 + i, z);
+          z = zn;
+        }
+      } else {
+        int z0 = coord(w.t0), z1 = coord(w.t0 + 1), z2 = coord(w.t0 + 2);
+        fill(&maps.k, w.t0, z0);
+        if (n > 1 && ok) fill(&maps.k, w.t0 + 1, z1);
+        for (int i = 0; i < n && ok; ++i) {
+          const int z3 = coord(w.t0 + i + 3);
+          fill(&maps.v, w.t0 + i, z0);
+          if (i + 2 < n && ok) fill(&maps.k, w.t0 + i + 2, z2);
+          z0 = z1;
+          z1 = z2;
+          z2 = z3;
+        }
+      }
+    }
+    if (!ok) {  // no copy may land after the CTA has left
+      for (long long i = max(0LL, n_kv - NS); i < n_kv; ++i)
+        mbar_wait_bounded(&bars.kv_full[i % NS], static_cast<unsigned>((i / NS) & 1), kTcPollLimit, p.c.err);
+      if (n_q > 0) mbar_wait_bounded(&bars.q_full, static_cast<unsigned>((n_q - 1) & 1), kTcPollLimit, p.c.err);
+    }
+  } else if (warp == kTcMmaWarp) {
+    // ---- products, by one thread
+    if (lane == 0) {
+      const uint32_t idesc_qk = umma_idesc_bf16(kTcRows, kTcKeys, false);
+      const uint32_t idesc_pv = umma_idesc_bf16(kTcRows, D, true);
+      const uint32_t sq = smem_u32(smem + P::q), sr = smem_u32(smem + P::ring);
+      long long n_kv = 0;
+      int n_q = 0;
+      unsigned n_p[2] = {0u, 0u};
+      auto wait = [&](uint64_t* bar, unsigned parity) {
+        ok = ok && mbar_wait_bounded(bar, parity & 1u, kTcPollLimit, p.c.err);
+        tc_fence_after();
+        return ok;
+      };
+      // takes the ring's next buffer
+      auto next_kv = [&](int* st) {
+        *st = static_cast<int>(n_kv % NS);
+        const bool r = wait(&bars.kv_full[*st], static_cast<unsigned>(n_kv / NS));
+        ++n_kv;
+        return r;
+      };
+      auto qk = [&](int s, int st) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = static_cast<uint32_t>((k >> 2) * (kTcKeys * 128) + (k & 3) * 32);
+          umma_bf16(tmem + static_cast<uint32_t>(s) * kTcKeys,
+                    desc_sw128(sq + (PAIR ? s * P::tile : 0) + off, 16, 1024),
+                    desc_sw128(sr + st * P::tile + off, 16, 1024), idesc_qk, k > 0);
+        }
+        umma_commit(&bars.s_full[s]);
+      };
+      auto pv = [&](int s, int st, bool first) {
+#pragma unroll
+        for (int k = 0; k < kTcKeys / 16; ++k)
+          umma_bf16_ts(tmem + 256u + static_cast<uint32_t>(s) * D, tmem + static_cast<uint32_t>(s) * kTcKeys + k * 8,
+                       desc_sw128(sr + st * P::tile + k * 2048, kTcKeys * 128, 1024), idesc_pv, !(first && k == 0));
+      };
+      for (PieceWalk w(run); w.more() && ok; w.next(p)) {
+        const int n = w.t1 - w.t0;
+        if (!wait(&bars.q_full, static_cast<unsigned>(n_q))) break;
+        ++n_q;
+        int st_k, st_v;
+        if (PAIR) {
+          if (!next_kv(&st_k)) break;
+          qk(0, st_k);
+          qk(1, st_k);
+          umma_commit(&bars.kv_empty[st_k]);
+          if (n == 1) umma_commit(&bars.q_empty);
+          for (int i = 0; i < n; ++i) {
+            if (!next_kv(&st_v)) break;
+            if (!wait(&bars.p_full[0], n_p[0]++)) break;
+            pv(0, st_v, i == 0);
+            if (i + 1 < n) {
+              if (!next_kv(&st_k)) break;
+              qk(0, st_k);
+            } else {
+              umma_commit(&bars.o_done[0]);
+            }
+            if (!wait(&bars.p_full[1], n_p[1]++)) break;
+            pv(1, st_v, i == 0);
+            umma_commit(&bars.kv_empty[st_v]);
+            if (i + 1 < n) {
+              qk(1, st_k);
+              umma_commit(&bars.kv_empty[st_k]);
+              if (i + 2 == n) umma_commit(&bars.q_empty);
+            } else {
+              umma_commit(&bars.o_done[1]);
+            }
+          }
+        } else {
+          for (int i = 0; i < min(n, 2) && ok; ++i) {
+            if (!next_kv(&st_k)) break;
+            qk(i, st_k);
+            umma_commit(&bars.kv_empty[st_k]);
+          }
+          if (!ok) break;
+          if (n <= 2) umma_commit(&bars.q_empty);
+          for (int i = 0; i < n; ++i) {
+            const int s = i & 1;
+            if (!next_kv(&st_v)) break;
+            if (!wait(&bars.p_full[s], n_p[s]++)) break;
+            pv(s, st_v, i < 2);
+            umma_commit(&bars.kv_empty[st_v]);
+            if (i + 2 < n) {
+              if (!next_kv(&st_k)) break;
+              qk(s, st_k);
+              umma_commit(&bars.kv_empty[st_k]);
+              if (i + 3 == n) umma_commit(&bars.q_empty);
+            }
+          }
+          umma_commit(&bars.o_done[0]);
+        }
+        if (!ok) break;
+      }
+      if (!ok) {  // products in flight end before tensor memory is freed
+        umma_commit(&bars.drain);
+        mbar_wait_bounded(&bars.drain, 0, kTcPollLimit, p.c.err);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax of stream s, a thread per row
+    const int s = warp >> 2, sub = warp & 3;
+    const int r = sub * 32 + lane;  // row of the tile, tensor-memory lane
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(sub * 32) << 16);
+    const uint32_t t_s = lane_base + static_cast<uint32_t>(s) * kTcKeys;
+    const uint32_t t_o = lane_base + 256u + static_cast<uint32_t>(s) * D;
+    unsigned n_s = 0, n_piece = 0;
+    long long n_kv = 0;  // ring position of the piece's first buffer
+    bool wrote = false;
+    // after a wait that ran out a warp only keeps the CTA's barriers company
+    for (PieceWalk w(run); w.more(); w.next(p)) {
+      const AttendItem& it = w.it;
+      const int n = w.t1 - w.t0;
+      const int row0 = it.row0 + (PAIR ? s * tile_rows : 0);
+      const int rows = min(tile_rows, it.rows - (PAIR ? s * tile_rows : 0));  // <= 0: an empty second tile
+      const bool warp_live = sub * 32 < rows;
+      const int node = min((row0 + r) / p.c.G, max(it.len - 1, 0));
+      // keys below this are visible to every row of the piece
+      const int full_end = p.mask ? it.ctx : it.ctx + it.row0 / p.c.G + 1;
+      float m = -INFINITY, l = 0.f;
+      for (int i = PAIR ? 0 : s; i < n && ok; i += PAIR ? 1 : 2) {
+        const int t = w.t0 + i;
+        const bool first = i < 2 && (PAIR ? i == 0 : true);
+        const bool masked = (t + 1) * kTcKeys > full_end;
+        ok = mbar_wait_bounded(&bars.s_full[s], n_s & 1u, kTcPollLimit, p.c.err);
+        ++n_s;
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (masked && (!PAIR || s == 0)) {
+          // this tile's values: their buffer's place in the loader's order
+          const long long at = n_kv + (PAIR ? 2 * i + 1 : (n == 1 ? 1 : min(2 * i + 2, n + i)));
+          const int st = static_cast<int>(at % NS);
+          ok = mbar_wait_bounded(&bars.kv_full[st], static_cast<unsigned>((at / NS) & 1), kTcPollLimit, p.c.err);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          clean_values<D>(smem + P::ring + st * P::tile, it.kv_end - t * kTcKeys, r, &sh.bad[s]);
+        }
+        if (warp_live) {
+          // two passes over the scores, 32 columns at a time: the maximum, then
+          // P.  Reading the scores twice keeps a thread within its registers.
+          auto hide = [&](float* x, int c) {
+            if (!masked) return;
+            const uint32_t bits = visible_bits(p, it, node, t * kTcKeys + c);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!((bits >> j) & 1u)) x[j] = -INFINITY;
+          };
+          float x[2][32];
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          tmem_ld32_async(t_s, x[0]);
+#pragma unroll
+          for (int c = 0; c < kTcKeys / 32; ++c) {
+            tmem_ld_wait<32>(x[c & 1]);
+            if (c + 1 < kTcKeys / 32) tmem_ld32_async(t_s + (c + 1) * 32, x[(c + 1) & 1]);
+            hide(x[c & 1], c * 32);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[c & 1][j]);
+          }
+          tmem_ld32_async(t_s, x[0]);
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+          // the maximum in use may lag behind by 2^8, which fp32 sums and outputs hold easily
+          const bool move = top > m + kRescaleLog2 || (m == -INFINITY && top != -INFINITY);
+          float fix = 1.f;
+          if (move) {
+            fix = exp2_approx(m - top);
+            m = top;
+            l *= fix;
+          }
+          if (!first && __any_sync(0xffffffffu, move && r < rows)) {
+            float o[32];
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              tmem_ld32_async(t_o + c, o);
+              tmem_ld_wait<32>(o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] *= fix;
+              tmem_st32(t_o + c, reinterpret_cast<const uint32_t*>(o));
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : m;
+          // P is rounded to bf16 for the tensor cores; the sum takes the
+          // rounded values, so that the weights still add up to one
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < kTcKeys / 32; ++c) {
+            tmem_ld_wait<32>(x[c & 1]);
+            if (c + 1 < kTcKeys / 32) tmem_ld32_async(t_s + (c + 1) * 32, x[(c + 1) & 1]);
+            hide(x[c & 1], c * 32);
+            uint32_t w16[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float p0 = exp2_approx(fmaf(x[c & 1][2 * j], p.scale_log2, -base));
+              const float p1 = exp2_approx(fmaf(x[c & 1][2 * j + 1], p.scale_log2, -base));
+              const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+              w16[j] = *reinterpret_cast<const uint32_t*>(&b);
+              sum[j & 3] += __uint_as_float(w16[j] << 16) + __uint_as_float(w16[j] & 0xffff0000u);
+            }
+            // columns 16 c .. of P lie over scores that are read already
+            tmem_st16(t_s + c * 16, w16);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full[s]);
+      }
+      n_kv += 2LL * n;
+      // ---- result of the piece
+      const bool starts = w.t0 == 0, whole = starts && w.t1 == it.nt;
+      if (!PAIR) {
+        sh.ml[s][r] = make_float2(m, l);
+        named_bar_sync(1, 256);
+      }
+      ok = ok && mbar_wait_bounded(&bars.o_done[PAIR ? s : 0], n_piece & 1u, kTcPollLimit, p.c.err);
+      ++n_piece;
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        tc_fence_after();
+        float w0 = 1.f, w1 = 0.f;
+        if (!PAIR) {
+          const float2 a = sh.ml[0][r], b = sh.ml[1][r];
+          m = fmaxf(a.x, b.x);
+          const float base = m == -INFINITY ? 0.f : m;
+          w0 = exp2_approx(a.x - base);
+          w1 = exp2_approx(b.x - base);
+          l = a.y * w0 + b.y * w1;
+        }
+        const int bad = PAIR ? sh.bad[0] : sh.bad[0] | sh.bad[1];
+        const int slot0 = max(w.t0 * kTcKeys, full_end / kTcKeys * kTcKeys);
+        const int slot1 = min(w.t1 * kTcKeys, it.kv_end);
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        const int g_row = row0 + r, nd = g_row / p.c.G, g = g_row - nd * p.c.G;
+        constexpr int NC = PAIR ? D : D / 2;  // columns of this warp group
+        const int c0 = PAIR ? 0 : s * NC;
+        const int rr = r + (PAIR ? s * tile_rows : 0);
+        const long long slot_row =
+            static_cast<long long>(piece_slot(static_cast<int>(blockIdx.x), starts)) * p.rows_step + rr;
+        if (!whole && r < rows && c0 == 0)
+          *reinterpret_cast<float2*>(p.part_ml + slot_row * 2) = make_float2(m, l);
+        if (warp_live) {
+#pragma unroll 1
+          for (int c = 0; c < NC; c += 32) {
+            float o[32], o1[32];
+            if (PAIR) {
+              tmem_ld32_async(t_o + c, o);
+              tmem_ld_wait<32>(o);
+            } else {
+              tmem_ld32_async(lane_base + 256u + c0 + c, o);
+              tmem_ld32_async(lane_base + 256u + D + c0 + c, o1);
+              tmem_ld_wait<32>(o);
+              tmem_ld_wait<32>(o1);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = n > 1 ? fmaf(o1[j], w1, o[j] * w0) : o[j] * w0;
+            }
+            if (r < rows) {
+              if (bad) add_nonfinite<32>(p, it, node, slot0, slot1, D, c0 + c, o);
+              if (whole) {
+                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
+                                     (((static_cast<long long>(it.l) * p.c.B + it.b) * p.c.n_max + nd) * p.c.nq +
+                                      it.kh * p.c.G + g) * D + c0 + c;
+#pragma unroll
+                for (int j = 0; j < 32; j += 8) {
+                  uint32_t u[4];
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    // a row that sees nothing is zero, whatever P V holds
+                    const float y0 = inv == 0.f ? 0.f : o[j + 2 * e] * inv, y1 = inv == 0.f ? 0.f : o[j + 2 * e + 1] * inv;
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(y0, y1);
+                    u[e] = *reinterpret_cast<const uint32_t*>(&b);
+                  }
+                  *reinterpret_cast<uint4*>(dst + j) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+              } else {
+                float* dst = p.part_o + slot_row * D + c0 + c;
+#pragma unroll
+                for (int j = 0; j < 32; j += 4)
+                  *reinterpret_cast<float4*>(dst + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+              }
+            }
+          }
+        }
+        if (starts && !whole) {
+          if (tid == 0) write_meta(p, run, true, it, run.first + run.tiles - w.left);
+          wrote = true;
+        }
+        tc_fence_before();
+      }
+      // outputs and flags are read: the next piece may overwrite them
+      named_bar_sync(1, 256);
+      if (tid == 0) sh.bad[0] = sh.bad[1] = 0;
+      named_bar_sync(1, 256);
+    }
+    if (!wrote && tid == 0) write_meta(p, run, false, run.it, 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kTcMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tc_map_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
+  }();
+  return fn;
+}
+
+// q as (D, n_q, node, layer x sequence) with boxes of 64 x G x nodes x 1, keys
+// and values as (D, slot of the page, layer x page x head) with boxes of 64 x
+// page rows x 1; what lies outside reads as zeros.
+cudaError_t encode_maps(const AttendParams& p, int D, int nodes, TcMaps* m) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = tc_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const PagedParams& c = p.c;
+  const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
+  const cuuint64_t qd[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(c.nq), static_cast<cuuint64_t>(c.n_max),
+                            static_cast<cuuint64_t>(c.Lc) * static_cast<cuuint64_t>(c.B)};
+  const cuuint64_t qs[3] = {row, row * c.nq, row * c.nq * c.n_max};
+  const cuuint32_t qb[4] = {64, static_cast<cuuint32_t>(c.G), static_cast<cuuint32_t>(nodes), 1};
+  if (enc(&m->q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p.q), qd, qs, qb, estr,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  const cuuint64_t kd[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(c.ps),
+                            static_cast<cuuint64_t>(c.l0 + c.Lc) * static_cast<cuuint64_t>(c.n_pages) *
+                                static_cast<cuuint64_t>(c.nkv)};
+  const cuuint64_t ks[2] = {row, row * c.ps};
+  const cuuint32_t kb[3] = {64, static_cast<cuuint32_t>(std::min(c.ps, kTcKeys)), 1};
+  auto kv = [&](CUtensorMap* map, void* base) {
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, kd, ks, kb, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  return kv(&m->k, c.k_pages) && kv(&m->v, c.v_pages) ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int D, bool PAIR>
+constexpr int tc_smem() { return TcPlan<D, PAIR>::shared + static_cast<int>(sizeof(TcShared)); }
+
+template <int D, bool PAIR>
+cudaError_t launch_tc(const AttendParams& p, cudaStream_t s) {
+  TcMaps maps;
+  const cudaError_t e = encode_maps(p, D, p.rows_step / (PAIR ? 2 : 1) / p.c.G, &maps);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.n_cta), 1, 1);
+  cfg.blockDim = dim3(kTcThreads, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(tc_smem<D, PAIR>());
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attend_tc_kernel<D, PAIR>, p, maps);
+}
+
+template <int D, bool PAIR>
+cudaError_t allow_tc() {
+  return cudaFuncSetAttribute(attend_tc_kernel<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              tc_smem<D, PAIR>());
+}
+
+}  // namespace
+
+// Nodes of a row tile; the call takes two row tiles at a time when its nodes
+// do not fit one.
+void attend_tc_rows(int G, int n_max, int* rows_step, int* kt) {
+  const int nodes = kTcRows / G;
+  *rows_step = n_max <= nodes ? n_max * G : 2 * nodes * G;
+  *kt = kTcKeys;
+}
+
+cudaError_t attend_tc_prepare() {
+  cudaError_t e = allow_tc<64, false>();
+  if (e == cudaSuccess) e = allow_tc<64, true>();
+  if (e == cudaSuccess) e = allow_tc<128, false>();
+  if (e == cudaSuccess) e = allow_tc<128, true>();
+  return e;
+}
+
+cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, cudaStream_t s) {
+  const bool pair = p.c.n_max > kTcRows / p.c.G;
+  if (head_dim == 64) return pair ? launch_tc<64, true>(p, s) : launch_tc<64, false>(p, s);
+  return pair ? launch_tc<128, true>(p, s) : launch_tc<128, false>(p, s);
+}
+
+}  // namespace sfa
