@@ -447,7 +447,9 @@ SFA_API size_t sfa_kv_attend_workspace_bytes(const sfa_handle* h, int n_max);
  * among them.  q [layer_count][batch][n_max][n_q][d], out [layer_count][batch]
  * [n_max][hidden], both in_dtype (out is thus the attention output that
  * SFA_OUT_ADD_BF16 or SFA_OUT_ADD_F32 adds to).  SFA_ERR_UNSUPPORTED for a mask
- * with n_max > SFA_TREE_MAX, layer_count * batch * n_max * n_q > 2^31 - 1.
+ * with n_max > SFA_TREE_MAX, batch > 4096, layer_count * batch * n_max * n_q >
+ * 2^31 - 1, or more than 2^30 tiles of 64 keys over all layers, sequences, KV
+ * heads and row tiles at max_pages full pages.
  * SFA_ERR_WORKSPACE if workspace is too small. */
 SFA_API int sfa_kv_attend(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begin, int layer_count,
                           const void* q, int n_max, const int* lens, const int* ctx_lens,

@@ -222,6 +222,10 @@ def sfa_abi_version() -> int:
 
 def _stream_ptr(stream) -> int:
     if stream is None:
+        # the current stream's handle without a Stream object, where torch has it
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return int(raw(torch.cuda.current_device()))
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -611,40 +615,35 @@ class SfaRope:
         self._arr = (None if self.inv_freq is None
                      else (ctypes.c_double * len(self.inv_freq))(*self.inv_freq))
         self.c = sfa_rope(self.style, self.dims, self.base, self._arr)
+        self.ref = ctypes.byref(self.c)
 
     def check(self, head_dim: int) -> None:
+        if self.inv_freq is None:
+            return
         need = (self.dims or head_dim) // 2
-        if self.inv_freq is not None and len(self.inv_freq) < need:
+        if len(self.inv_freq) < need:
             raise ValueError(f"inv_freq has {len(self.inv_freq)} values, needs {need}")
 
 
-def _ints(t, name: str, shape, device) -> Optional[int]:
-    """Pointer of a contiguous int32 tensor of exactly `shape` on `device`."""
-    if t is None:
-        return None
-    p = _dev(t, name, torch.int32)
+def _need(t, name: str, dtype, shape, index: int) -> int:
+    """Pointer of a contiguous CUDA tensor of exactly this dtype and shape on
+    device `index`.  One test in the usual case: these calls run once per layer
+    and step, where a microsecond of checks is a microsecond of the step."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == index and t.is_contiguous() and _is_cuda_tensor(t)):
+        return t.data_ptr()
+    _dev(t, name, dtype)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return p
+    raise ValueError(f"{name} is on device {t.get_device()}, not on {index}")
 
 
-def _rows(t, name: str, shape, dtype, device) -> int:
-    p = _dev(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return p
-
-
-def _call_on(device, stream, fn, *args) -> int:
-    """fn(*args, stream) with `device` current; stream None is that device's
-    current stream."""
-    if device.type != "cuda" or device.index is None or device.index == torch.cuda.current_device():
+def _call_on(index: int, stream, fn, *args) -> int:
+    """fn(*args, stream) with device `index` current; stream None is that
+    device's current stream."""
+    if index < 0 or index == torch.cuda.current_device():
         return fn(*args, _stream_ptr(stream))
-    with torch.cuda.device(device):
+    with torch.cuda.device(index):
         return fn(*args, _stream_ptr(stream))
 
 
@@ -658,17 +657,18 @@ def sfa_tree_plan(h: Handle, parents: torch.Tensor, ctx_lens: torch.Tensor,
     if not isinstance(parents, torch.Tensor) or parents.dim() != 2:
         raise ValueError("parents must be a [batch, n] tensor")
     B, n = parents.shape
-    dev = parents.device
-    pp = _ints(parents, "parents", (B, n), dev)
-    cp, lp = _ints(ctx_lens, "ctx_lens", (B,), dev), _ints(lens, "lens", (B,), dev)
+    dev, i32 = parents.get_device(), torch.int32
     words = (n + 31) // 32
     if positions is None:
-        positions = _zeros_for((B, n), torch.int32, dev, stream)
+        positions = _zeros_for((B, n), i32, parents.device, stream)
     if mask is None:
-        mask = _zeros_for((B, n, words), torch.int32, dev, stream)
-    rc = _call_on(dev, stream, load_library().sfa_tree_plan, h.ptr, pp, n, lp, cp, B,
-                  _ints(positions, "positions", (B, n), dev),
-                  _ints(mask, "mask", (B, n, words), dev))
+        mask = _zeros_for((B, n, words), i32, parents.device, stream)
+    rc = _call_on(dev, stream, load_library().sfa_tree_plan, h.ptr,
+                  _need(parents, "parents", i32, (B, n), dev), n,
+                  None if lens is None else _need(lens, "lens", i32, (B,), dev),
+                  _need(ctx_lens, "ctx_lens", i32, (B,), dev), B,
+                  _need(positions, "positions", i32, (B, n), dev),
+                  _need(mask, "mask", i32, (B, n, words), dev))
     if rc != SFA_OK:
         raise SfaError(rc, "sfa_tree_plan")
     return positions, mask
@@ -707,27 +707,32 @@ class SfaPagedCache:
         self.handle = handle
         if k_pages.dim() != 5 or page_table.dim() != 2:
             raise ValueError("k_pages must be [L, n_pages, n_kv, page_size, d] and page_table [batch, max_pages]")
-        self.device = k_pages.device
+        self.device, dev = k_pages.device, k_pages.get_device()
         self.n_pages, self.page_size = k_pages.shape[1], k_pages.shape[3]
         self.batch, self.max_pages = page_table.shape
         shape = (c.n_layers, self.n_pages, c.n_kv_heads, self.page_size, c.head_dim)
-        kp = _rows(k_pages, "k_pages", shape, c.torch_dtype, self.device)
-        vp = _rows(v_pages, "v_pages", shape, c.torch_dtype, self.device)
-        tp = _ints(page_table, "page_table", page_table.shape, self.device)
+        kp = _need(k_pages, "k_pages", c.torch_dtype, shape, dev)
+        vp = _need(v_pages, "v_pages", c.torch_dtype, shape, dev)
+        tp = _need(page_table, "page_table", torch.int32, page_table.shape, dev)
         self.k_pages, self.v_pages, self.page_table = k_pages, v_pages, page_table
         self.c = sfa_kv_cache(kp, vp, self.n_pages, self.page_size, self.max_pages, tp)
-        self._ws = {}
+        self._ws, self._ws_need = {}, {}
+        # what the calls, made once per layer and step, look up
         self._ref = ctypes.byref(self.c)
+        self._index, self._dtype, self._lens_shape = dev, c.torch_dtype, (self.batch,)
+        self._q_tail, self._kv_tail = (c.n_q_heads, c.head_dim), (c.n_kv_heads, c.head_dim)
+        lib = load_library()
+        self._append_fn, self._attend_fn, self._accept_fn = lib.sfa_kv_append, lib.sfa_kv_attend, lib.sfa_kv_accept
 
-    def _lens(self, ctx_lens, lens):
-        B = self.batch
-        return (_ints(ctx_lens, "ctx_lens", (B,), self.device),
-                _ints(lens, "lens", (B,), self.device))
+    def _len_ptr(self, t, name: str) -> Optional[int]:
+        return None if t is None else _need(t, name, torch.int32, self._lens_shape, self._index)
 
     def _workspace(self, n: int, stream) -> torch.Tensor:
         """This stream's workspace, grown to what n new tokens need."""
-        need = sfa_kv_attend_workspace_bytes(self.handle, n)
-        key = _stream_ptr(stream) if stream is not None else _stream_ptr(torch.cuda.current_stream(self.device))
+        need = self._ws_need.get(n)
+        if need is None:
+            need = self._ws_need[n] = sfa_kv_attend_workspace_bytes(self.handle, n)
+        key = _stream_ptr(stream)
         ws = self._ws.get(key)
         if ws is None or ws.numel() < need:
             if ws is not None and isinstance(stream, torch.cuda.Stream):
@@ -746,32 +751,31 @@ class SfaPagedCache:
         """Rotated keys and values of the new tokens into their pages; returns
         (q_out, k_out), the rotated queries (a new tensor unless given; None
         without q) and keys (None unless given)."""
-        cfg, dev, B = self.handle.cfg, self.device, self.batch
         if k.dim() != 5:
             raise ValueError("k must be [layers, batch, n, n_kv, d]")
+        dev, dt, B = self._index, self._dtype, self.batch
         Lc, n = k.shape[0], k.shape[2]
-        kv = (Lc, B, n, cfg.n_kv_heads, cfg.head_dim)
-        qs = (Lc, B, n, cfg.n_q_heads, cfg.head_dim)
-        cp, lp = self._lens(ctx_lens, lens)
-        kp, vp = _rows(k, "k", kv, cfg.torch_dtype, dev), _rows(v, "v", kv, cfg.torch_dtype, dev)
+        rows = (Lc, B, n)
+        kv, qs = rows + self._kv_tail, rows + self._q_tail
         qp = qo = ko = None
         if q is not None:
-            qp = _rows(q, "q", qs, cfg.torch_dtype, dev)
+            qp = _need(q, "q", dt, qs, dev)
             if q_out is None:
-                q_out = torch.empty_like(q) if lens is None else _zeros_for(qs, q.dtype, dev, stream)
-                if isinstance(stream, torch.cuda.Stream):
-                    q_out.record_stream(stream)
-            qo = _rows(q_out, "q_out", qs, cfg.torch_dtype, dev)
+                q_out = _zeros_for(qs, dt, self.device, stream)
+            qo = _need(q_out, "q_out", dt, qs, dev)
         elif q_out is not None:
             raise ValueError("q_out needs q")
         if k_out is not None:
-            ko = _rows(k_out, "k_out", kv, cfg.torch_dtype, dev)
-        pp = _ints(positions, "positions", (B, n), dev)
+            ko = _need(k_out, "k_out", dt, kv, dev)
+        rp = None
         if rope is not None:
-            rope.check(cfg.head_dim)
-        rc = _call_on(dev, stream, load_library().sfa_kv_append, self.handle.ptr, self._ref, layer_begin, Lc,
-                      qp, kp, vp, n, lp, cp, pp, None if rope is None else ctypes.byref(rope.c), B,
-                      qo, ko)
+            rope.check(self._kv_tail[1])
+            rp = rope.ref
+        rc = _call_on(dev, stream, self._append_fn, self.handle.ptr, self._ref, layer_begin, Lc, qp,
+                      _need(k, "k", dt, kv, dev), _need(v, "v", dt, kv, dev), n,
+                      self._len_ptr(lens, "lens"), _need(ctx_lens, "ctx_lens", torch.int32, (B,), dev),
+                      None if positions is None else _need(positions, "positions", torch.int32, (B, n), dev),
+                      rp, B, qo, ko)
         if rc != SFA_OK:
             raise SfaError(rc, "sfa_kv_append")
         return q_out, k_out
@@ -784,24 +788,26 @@ class SfaPagedCache:
         out [layers, B, n, hidden] in the input dtype.  mask [B, n, words] as of
         sfa_tree_plan, or None: every new token sees those before it.  Rows past
         lens keep what out held (a new out is zero there)."""
-        cfg, dev, B = self.handle.cfg, self.device, self.batch
         if q.dim() != 5:
             raise ValueError("q must be [layers, batch, n, n_q, d]")
+        dev, dt, B = self._index, self._dtype, self.batch
         Lc, n = q.shape[0], q.shape[2]
-        qp = _rows(q, "q", (Lc, B, n, cfg.n_q_heads, cfg.head_dim), cfg.torch_dtype, dev)
-        cp, lp = self._lens(ctx_lens, lens)
-        mp = _ints(mask, "mask", (B, n, (n + 31) // 32), dev)
+        rows = (Lc, B, n)
+        qp = _need(q, "q", dt, rows + self._q_tail, dev)
+        cp = _need(ctx_lens, "ctx_lens", torch.int32, self._lens_shape, dev)
+        mp = None if mask is None else _need(mask, "mask", torch.int32, (B, n, (n + 31) // 32), dev)
+        hidden = self._q_tail[0] * self._q_tail[1]
         if out is None:
-            out = _zeros_for((Lc, B, n, cfg.hidden), cfg.torch_dtype, dev, stream)
-        op = _rows(out, "out", (Lc, B, n, cfg.hidden), cfg.torch_dtype, dev)
+            out = _zeros_for(rows + (hidden,), dt, self.device, stream)
+        op = _need(out, "out", dt, rows + (hidden,), dev)
         if n == 0:
             return out
-        ws = self._workspace(n, stream) if workspace is None else workspace
-        wp = _dev(ws, "workspace", torch.uint8)
-        if ws.device != dev:
-            raise ValueError(f"workspace is on {ws.device}, not on {dev}")
-        rc = _call_on(dev, stream, load_library().sfa_kv_attend, self.handle.ptr, self._ref, layer_begin, Lc,
-                      qp, n, lp, cp, mp, B, op, wp, ws.numel())
+        if workspace is None:
+            workspace = self._workspace(n, stream)
+        size = workspace.numel()
+        rc = _call_on(dev, stream, self._attend_fn, self.handle.ptr, self._ref, layer_begin, Lc, qp, n,
+                      self._len_ptr(lens, "lens"), cp, mp, B, op,
+                      _need(workspace, "workspace", torch.uint8, (size,), dev), size)
         if rc != SFA_OK:
             raise SfaError(rc, "sfa_kv_attend")
         return out
@@ -813,13 +819,11 @@ class SfaPagedCache:
         then adds n_accept to ctx_lens."""
         if path.dim() != 2:
             raise ValueError("path must be [batch, n]")
-        B, n = self.batch, path.shape[1]
-        pp = _ints(path, "path", (B, n), self.device)
-        cp, np_ = self._lens(ctx_lens, n_accept)
-        if np_ is None:
-            raise ValueError("n_accept must be a CUDA tensor")
-        rc = _call_on(self.device, stream, load_library().sfa_kv_accept, self.handle.ptr, self._ref, layer_begin,
-                      layer_count, pp, n, np_, cp, B)
+        dev, B, n = self._index, self.batch, path.shape[1]
+        rc = _call_on(dev, stream, self._accept_fn, self.handle.ptr, self._ref, layer_begin, layer_count,
+                      _need(path, "path", torch.int32, (B, n), dev), n,
+                      _need(n_accept, "n_accept", torch.int32, (B,), dev),
+                      _need(ctx_lens, "ctx_lens", torch.int32, (B,), dev), B)
         if rc != SFA_OK:
             raise SfaError(rc, "sfa_kv_accept")
 

@@ -812,6 +812,11 @@ int sfa_kv_attend(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begi
       static_cast<long long>(layer_count) * batch * c->n_q_heads > 0x7fffffffLL / n_max)
     return SFA_ERR_UNSUPPORTED;
   const AttendPlan a = attend_plan(c->in_dtype, c->head_dim, p.c.G, n_max, h->n_sm);
+  // the kernels count key tiles in 32 bits
+  const double tiles = static_cast<double>(layer_count) * batch * c->n_kv_heads *
+                       ((static_cast<long long>(n_max) * p.c.G + a.rows_step - 1) / a.rows_step) *
+                       ((static_cast<long long>(p.c.max_pages) * p.c.ps + a.kt - 1) / a.kt);
+  if (tiles > 1073741824.0) return SFA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < a.total) return SFA_ERR_WORKSPACE;
   if (!on_device(h)) return SFA_ERR_INVALID_ARG;
   unsigned char* ws = static_cast<unsigned char*>(workspace);

@@ -60,9 +60,9 @@ struct AttendItem {
 struct AttendRun {
   AttendItem it;      // item of the first tile
   int tile;           // its first tile
-  long long first;    // global index of the first tile
-  long long tiles;    // tiles of this CTA
-  long long chunk;    // tiles of every CTA but the last ones
+  int first;          // global index of the first tile
+  int tiles;          // tiles of this CTA
+  int chunk;          // tiles of every CTA but the last ones
 };
 
 __device__ __forceinline__ int row_tiles(const AttendParams& p, int len) {
@@ -102,116 +102,118 @@ __device__ __forceinline__ void next_item(const AttendParams& p, AttendItem& it)
   set_item(p, it);
 }
 
-// This CTA's run, by all NT threads.  s_pre: shared scratch of B + 1 long longs.
-template <int NT>
-__device__ __forceinline__ void find_run(const AttendParams& p, long long* s_pre, AttendRun* s_run) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int B = p.c.B;
-  const int most = row_tiles(p, p.c.n_max);
-  if (p.mask || most <= 8) {
-    for (int b = tid; b < B; b += NT) {
-      const SeqLens s = seq_lens(p.c, b, blockIdx.x == 0);
-      long long n = 0;
-      const int nrt = row_tiles(p, s.len);
-      if (p.mask)
-        n = static_cast<long long>(nrt) * ((s.ctx + s.len + p.kt - 1) / p.kt);
-      else
-        for (int rt = 0; rt < nrt; ++rt) n += (kv_end_of(p, s.ctx, s.len, rt) + p.kt - 1) / p.kt;
-      s_pre[b] = n * p.c.nkv;
+__device__ __forceinline__ int tiles_of(const AttendParams& p, int ctx, int len, int rt) {
+  return (kv_end_of(p, ctx, len, rt) + p.kt - 1) / p.kt;
+}
+
+__device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += up;
+  }
+  return v;
+}
+
+// Tiles of one KV head of sequence s, by one thread (few row tiles).
+__device__ __forceinline__ int seq_tiles(const AttendParams& p, const SeqLens& s) {
+  const int nrt = row_tiles(p, s.len);
+  if (p.mask) return nrt * ((s.ctx + s.len + p.kt - 1) / p.kt);
+  int n = 0;
+  for (int rt = 0; rt < nrt; ++rt) n += tiles_of(p, s.ctx, s.len, rt);
+  return n;
+}
+
+// The same by a whole warp, for causal calls of many row tiles.
+__device__ __forceinline__ int seq_tiles_warp(const AttendParams& p, const SeqLens& s, int lane) {
+  const int nrt = row_tiles(p, s.len);
+  int n = 0;
+  for (int rt = lane; rt < nrt; rt += 32) n += tiles_of(p, s.ctx, s.len, rt);
+  return __reduce_add_sync(0xffffffffu, n);
+}
+
+// This CTA's run, worked out by every calling warp for itself: prefix sums over
+// the sequences by shuffles, so that no warp waits for another.  The host
+// bounds the call's tiles by 2^31.
+__device__ __forceinline__ AttendRun find_run(const AttendParams& p, bool latch) {
+  const int lane = threadIdx.x & 31;
+  const int B = p.c.B, nkv = p.c.nkv;
+  const bool wide = !p.mask && row_tiles(p, p.c.n_max) > 8;
+  const int per = (B + 31) >> 5, b0 = min(B, lane * per), b1 = min(B, b0 + per);
+  int mine = 0, layer;  // tiles of one KV head of this lane's sequences; of all
+  if (wide) {
+    layer = 0;
+    for (int b = 0; b < B; ++b) layer += seq_tiles_warp(p, seq_lens(p.c, b, latch && lane == 0), lane);
+  } else {
+    for (int b = b0; b < b1; ++b) mine += seq_tiles(p, seq_lens(p.c, b, latch));
+    layer = __reduce_add_sync(0xffffffffu, mine);
+  }
+  AttendRun r;
+  const int total = layer * nkv * p.c.Lc;
+  r.chunk = max(p.min_tiles, (total + p.n_cta - 1) / p.n_cta);
+  const long long first = static_cast<long long>(blockIdx.x) * r.chunk;
+  r.first = static_cast<int>(min(first, static_cast<long long>(total)));
+  r.tiles = min(r.chunk, total - r.first);
+  r.tile = 0;
+  if (r.tiles <= 0) return r;
+  const int l = r.first / (layer * nkv);
+  int rem = r.first - l * layer * nkv;  // tile within the layer
+  // the sequence: prefix sums count one KV head, the order within a sequence is row tile, KV head
+  SeqLens s;
+  int b = 0;
+  if (wide) {
+    for (;; ++b) {
+      s = seq_lens(p.c, b, false);
+      const int n = seq_tiles_warp(p, s, lane) * nkv;
+      if (rem < n) break;
+      rem -= n;
     }
   } else {
-    for (int b = warp; b < B; b += NT / 32) {
-      const SeqLens s = seq_lens(p.c, b, blockIdx.x == 0);
-      const int nrt = row_tiles(p, s.len);
-      long long n = 0;
-      for (int rt = lane; rt < nrt; rt += 32) n += (kv_end_of(p, s.ctx, s.len, rt) + p.kt - 1) / p.kt;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-      if (lane == 0) s_pre[b] = n * p.c.nkv;
+    const int inc = warp_scan(mine, lane) * nkv;
+    const int src = __ffs(__ballot_sync(0xffffffffu, inc > rem)) - 1;  // the lane whose sequences hold it
+    rem -= __shfl_sync(0xffffffffu, inc - mine * nkv, src);
+    b = src * per;
+    if (per > 1) {
+      for (;; ++b) {
+        s = seq_lens(p.c, b, false);
+        const int n = seq_tiles(p, s) * nkv;
+        if (rem < n) break;
+        rem -= n;
+      }
+    } else {
+      s = seq_lens(p.c, b, false);
     }
   }
-  __syncthreads();
-  if (warp == 0) {
-    // exclusive prefix sums: a run of sequences per lane, then a warp scan
-    const int per = (B + 31) / 32;
-    const int b0 = min(B, lane * per), b1 = min(B, b0 + per);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += s_pre[b];
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += up;
-    }
-    const long long layer = __shfl_sync(0xffffffffu, inc, 31);
-    long long at = inc - mine;
-    for (int b = b0; b < b1; ++b) {
-      const long long n = s_pre[b];
-      s_pre[b] = at;
-      at += n;
-    }
-    if (lane == 31) s_pre[B] = layer;
-    __syncwarp();
-    const long long total = layer * p.c.Lc;
-    const long long chunk = max(static_cast<long long>(p.min_tiles), (total + p.n_cta - 1) / p.n_cta);
-    const long long first = static_cast<long long>(blockIdx.x) * chunk;
-    const long long tiles = max(0LL, min(chunk, total - first));
-    AttendRun r;
-    r.first = first;
-    r.tiles = tiles;
-    r.chunk = chunk;
-    if (tiles > 0) {
-      const int l = static_cast<int>(first / layer);
-      long long rem = first - l * layer;
-      int lo = 0, hi = B - 1;  // last sequence whose prefix is <= rem (one with tiles: empty ones share the next's prefix)
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s_pre[mid] <= rem) lo = mid;
-        else hi = mid - 1;
+  r.it.l = l;
+  r.it.b = b;
+  r.it.ctx = s.ctx;
+  r.it.len = s.len;
+  const int nrt = row_tiles(p, s.len);
+  int rt = 0, nt = 0;
+  if (p.mask) {
+    nt = (s.ctx + s.len + p.kt - 1) / p.kt;
+    rt = rem / (nt * nkv);
+    rem -= rt * nt * nkv;
+  } else {
+    for (int base = 0; base < nrt; base += 32) {  // the row tile that holds the remainder, 32 at a time
+      const int t = base + lane < nrt ? tiles_of(p, s.ctx, s.len, base + lane) : 0;
+      const int inc = warp_scan(t, lane) * nkv;
+      const unsigned hit = __ballot_sync(0xffffffffu, inc > rem);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        rt = base + src;
+        nt = __shfl_sync(0xffffffffu, t, src);
+        rem -= __shfl_sync(0xffffffffu, inc, src) - nt * nkv;
+        break;
       }
-      rem -= s_pre[lo];
-      r.it.l = l;
-      r.it.b = lo;
-      const SeqLens s = seq_lens(p.c, lo, false);
-      r.it.ctx = s.ctx;
-      r.it.len = s.len;
-      const int nrt = row_tiles(p, s.len);
-      int rt = 0, nt = 0;
-      if (p.mask) {
-        nt = (s.ctx + s.len + p.kt - 1) / p.kt;
-        const long long per_rt = static_cast<long long>(nt) * p.c.nkv;
-        rt = static_cast<int>(rem / per_rt);
-        rem -= rt * per_rt;
-      } else {
-        for (int base = 0; base < nrt; base += 32) {  // the row tile that holds the remainder, 32 at a time
-          const int mine_rt = base + lane;
-          const int t = mine_rt < nrt ? (kv_end_of(p, s.ctx, s.len, mine_rt) + p.kt - 1) / p.kt : 0;
-          const long long n = static_cast<long long>(t) * p.c.nkv;
-          long long inc2 = n;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const long long up = __shfl_up_sync(0xffffffffu, inc2, o);
-            if (lane >= o) inc2 += up;
-          }
-          const unsigned hit = __ballot_sync(0xffffffffu, inc2 > rem);
-          if (hit) {
-            const int src = __ffs(hit) - 1;
-            rt = base + src;
-            nt = __shfl_sync(0xffffffffu, t, src);
-            rem -= __shfl_sync(0xffffffffu, inc2 - n, src);
-            break;
-          }
-          rem -= __shfl_sync(0xffffffffu, inc2, 31);
-        }
-      }
-      r.it.rt = rt;
-      r.it.kh = static_cast<int>(rem / nt);
-      r.tile = static_cast<int>(rem - static_cast<long long>(r.it.kh) * nt);
-      set_item(p, r.it);
+      rem -= __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (lane == 0) *s_run = r;
   }
-  __syncthreads();
+  r.it.rt = rt;
+  r.it.kh = rem / nt;
+  r.tile = rem - r.it.kh * nt;
+  set_item(p, r.it);
+  return r;
 }
 
 // Partial result slot of a piece: a CTA has at most one piece that continues an
@@ -220,11 +222,11 @@ __device__ __forceinline__ int piece_slot(int cta, bool starts) { return cta * 2
 
 // Written once per run by one thread: the split item that this run starts, if any.
 __device__ __forceinline__ void write_meta(const AttendParams& p, const AttendRun& r, bool starts_split,
-                                           const AttendItem& it, long long item_first) {
+                                           const AttendItem& it, int item_first) {
   SplitMeta m = {};
   m.last_cta = -1;
   if (starts_split) {
-    m.last_cta = static_cast<int>((item_first + it.nt - 1) / r.chunk);
+    m.last_cta = (item_first + it.nt - 1) / r.chunk;
     m.l = it.l;
     m.b = it.b;
     m.kh = it.kh;

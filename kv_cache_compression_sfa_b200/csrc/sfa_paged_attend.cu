@@ -69,20 +69,18 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attend_simt_kernel(const __gr
   using P = SimtPlan<T, D, RPW>;
   constexpr int DPL = D / 32;  // output elements of a lane
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ AttendRun s_run;
   pdl_trigger();
   pdl_wait();
-  find_run<kSimtThreads>(p, reinterpret_cast<long long*>(smem), &s_run);
-  const AttendRun run = s_run;
+  const AttendRun run = find_run(p, blockIdx.x == 0 && threadIdx.x < 32);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float* s_q = reinterpret_cast<float*>(smem + P::q);
   float* s_p = reinterpret_cast<float*>(smem + P::pr) + warp * kSimtKeys * RPW;
   AttendItem it = run.it;
-  long long left = run.tiles;
+  int left = run.tiles;
   int t0 = run.tile;
   bool wrote = false;
   while (left > 0) {
-    const int t1 = static_cast<int>(min(static_cast<long long>(it.nt), t0 + left));
+    const int t1 = min(it.nt, t0 + left);
     // q of the item's rows, scaled to log2 units
     for (int a = tid; a < P::R * (D / 4); a += kSimtThreads) {
       const int r = a / (D / 4), d4 = (a - r * (D / 4)) * 4;

@@ -1,7 +1,7 @@
 // sfa_paged_attend_tc.cu — attention of new tokens over the paged cache on the
 // 5th-generation tensor cores (bf16).
 //
-// A CTA walks its run of key tiles (sfa_paged.cuh) with ten warps:
+// A CTA walks its run of key tiles (sfa_paged.cuh) with ten working warps:
 //   warp 8     loads: q by one tensor copy per 64 columns, keys and values
 //              page by page into a ring of 128-key buffers;
 //   warp 9     issues the products: S = Q K^T (both operands in shared memory,
@@ -28,7 +28,12 @@
 namespace sfa {
 namespace {
 
-constexpr int kTcThreads = 320;
+constexpr int kTcThreads = 384;  // ten working warps; registers are dealt out to groups of four
+// Registers of a thread after the split: 256 x 208 + 128 x 80 = 63,488, within
+// the 384 x 168 = 64,512 of the launch.  A softmax thread keeps its row's 128
+// scores in registers.
+constexpr int kTcSoftmaxRegs = 208;
+constexpr int kTcOtherRegs = 80;
 constexpr int kTcLoadWarp = 8;
 constexpr int kTcMmaWarp = 9;
 constexpr int kTcKeys = 128;     // keys of a tile
@@ -59,7 +64,6 @@ struct TcBars {
 };
 
 struct TcShared {
-  AttendRun run;
   TcBars bars;
   float2 ml[2][kTcRows];  // maximum and sum of both streams' rows
   int bad[2];             // clean_values found elements that are not finite
@@ -120,24 +124,35 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
       "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
-      ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
-      "r"(taddr)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Two fp32 operations in one instruction, and a maximum of three.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 // Pieces of a run, the same walk in every role.
 struct PieceWalk {
   AttendItem it;
-  int t0, t1;
-  long long left;
+  int t0, t1, left;
   __device__ __forceinline__ explicit PieceWalk(const AttendRun& r) : it(r.it), t0(r.tile), t1(0), left(r.tiles) {
-    if (left > 0) t1 = static_cast<int>(min(static_cast<long long>(it.nt), t0 + left));
+    if (left > 0) t1 = min(it.nt, t0 + left);
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ void next(const AttendParams& p) {
@@ -145,57 +160,67 @@ struct PieceWalk {
     if (left <= 0) return;
     next_item(p, it);
     t0 = 0;
-    t1 = static_cast<int>(min(static_cast<long long>(it.nt), left));
+    t1 = min(it.nt, left);
   }
 };
 
-// Bit i: key col0 + i is visible to `node`.
-__device__ __forceinline__ uint32_t visible_bits(const AttendParams& p, const AttendItem& it, int node, int col0) {
-  auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };
-  if (!p.mask) return below(it.ctx + min(node + 1, it.len) - col0);
-  const int rel0 = col0 - it.ctx;
-  if (rel0 <= -32) return 0xffffffffu;
+// Visibility of tile t's keys to one row: keys below `end`, and of the new
+// tokens those of the row's mask words (tree).  The words are loaded before
+// the scores are waited for.
+struct RowMask {
+  uint32_t w[kTcKeys / 32 + 1];
+  int end, shift;
+};
+
+__device__ __forceinline__ RowMask row_mask(const AttendParams& p, const AttendItem& it, int node, int t) {
+  RowMask r;
+  r.end = p.mask ? it.ctx + it.len : it.ctx + min(node + 1, it.len);
+  const int rel = t * kTcKeys - it.ctx;
+  const int w0 = rel >> 5;
+  r.shift = rel & 31;
   const uint32_t* m = p.mask + (static_cast<long long>(it.b) * p.c.n_max + node) * p.words;
-  uint32_t bits;
-  if (rel0 < 0) {
-    bits = (m[0] << (-rel0)) | below(-rel0);
-  } else {
-    const int w = rel0 >> 5, sh = rel0 & 31;
-    const uint32_t lo = w < p.words ? m[w] : 0u;
-    const uint32_t hi = w + 1 < p.words ? m[w + 1] : 0u;
-    bits = __funnelshift_r(lo, hi, sh);
+#pragma unroll
+  for (int i = 0; i < kTcKeys / 32 + 1; ++i) {
+    r.w[i] = 0xffffffffu;  // the context
+    if (p.mask && w0 + i >= 0) r.w[i] = w0 + i < p.words ? m[w0 + i] : 0u;
   }
-  return bits & below(it.ctx + it.len - col0);
+  return r;
 }
 
-// The masked tiles' values: rows past the item's keys become zero, and
-// elements that are not finite too (a product with a zero weight would be NaN
-// in rows that do not see them); *bad is set if there were any.
+// Bit i: key t * 128 + 32 * c + i is visible.
+__device__ __forceinline__ uint32_t visible_bits(const RowMask& r, int t, int c) {
+  const int n = r.end - (t * kTcKeys + 32 * c);
+  const uint32_t below = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+  return below & __funnelshift_r(r.w[c], r.w[c + 1], r.shift);
+}
+
+// The masked tiles' values, by the 128 threads of a stream (tid 0..127): rows
+// from `rows` on (past the item's keys) become zero, and of the rows from `lo`
+// on, which some row does not see, elements that are not finite too (their
+// product with a zero weight would be NaN); *bad is set if there were any.
 template <int D>
-__device__ __forceinline__ void clean_values(unsigned char* v, int rows, int r, int* bad) {
+__device__ __forceinline__ void clean_values(unsigned char* v, int lo, int rows, int tid, int* bad) {
+  constexpr int CH = D / 8;  // 16-byte chunks of a row
+  lo = max(lo, 0);
   bool any = false;
+  for (int i = tid; i < (kTcKeys - lo) * CH; i += 128) {
+    const int r = lo + i / CH, c = i % CH;
+    uint4* at = reinterpret_cast<uint4*>(v + (c >> 3) * (kTcKeys * 128) + r * 128 + (c & 7) * 16);
+    if (r >= rows) {
+      *at = make_uint4(0u, 0u, 0u, 0u);
+      continue;
+    }
+    uint4 x = *at;
+    uint32_t* w = &x.x;
+    bool hit = false;
 #pragma unroll
-  for (int h = 0; h < D / 64; ++h) {
-    uint4* row = reinterpret_cast<uint4*>(v + h * (kTcKeys * 128) + r * 128);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      uint4* at = row + ((c + r) & 7);
-      if (r >= rows) {
-        *at = make_uint4(0u, 0u, 0u, 0u);
-        continue;
-      }
-      uint4 x = *at;
-      uint32_t* w = &x.x;
-      bool hit = false;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if ((w[i] & 0x7f80u) == 0x7f80u) { w[i] &= 0xffff0000u; hit = true; }
-        if ((w[i] & 0x7f800000u) == 0x7f800000u) { w[i] &= 0x0000ffffu; hit = true; }
-      }
-      if (hit) {
-        *at = x;
-        any = true;
-      }
+    for (int j = 0; j < 4; ++j) {
+      if ((w[j] & 0x7f80u) == 0x7f80u) { w[j] &= 0xffff0000u; hit = true; }
+      if ((w[j] & 0x7f800000u) == 0x7f800000u) { w[j] &= 0x0000ffffu; hit = true; }
+    }
+    if (hit) {
+      *at = x;
+      any = true;
     }
   }
   if (any) *bad = 1;
@@ -250,18 +275,18 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
     mbar_fence_init();
   }
   if (warp == kTcMmaWarp) tmem_alloc(&sh.tmem, kTmemCols);
+  tc_fence_before();
+  __syncthreads();  // barriers and tensor memory are set up
+  tc_fence_after();
   pdl_trigger();
   pdl_wait();
-  find_run<kTcThreads>(p, reinterpret_cast<long long*>(smem), &sh.run);
-  fence_proxy_async_smem();  // the scratch of find_run lies where the copies land
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const AttendRun run = sh.run;
+  const AttendRun run = find_run(p, blockIdx.x == 0 && warp == 0);
   const uint32_t tmem = sh.tmem;
   const int tile_rows = PAIR ? p.rows_step / 2 : p.rows_step;  // rows of one row tile
   bool ok = true;
 
+  if (warp >= kTcLoadWarp) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcOtherRegs));
   if (warp == kTcLoadWarp) {
     // ---- loads.  Buffer order is the order of use: PAIR K0 V0 K1 V1 ..,
     // else K0 K1 V0 K2 V1 ..  A lane copies one page's share of one 64-column
@@ -272,7 +297,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
     const int my_page = lane % ppt, my_half = lane / ppt;
     const unsigned box_off = static_cast<unsigned>(my_half * (kTcKeys * 128) + my_page * prow * 128);
     const int z_none = static_cast<int>(static_cast<long long>(p.c.nkv) * p.c.n_pages * (p.c.l0 + p.c.Lc));
-    long long n_kv = 0;   // buffers filled so far
+    unsigned n_kv = 0, st = 0, ring_turn = 0;  // buffers filled so far; the next one and its turn
     int n_q = 0;
     for (PieceWalk w(run); w.more() && ok; w.next(p)) {
       if (n_q > 0) ok = mbar_wait_bounded(&bars.q_empty, static_cast<unsigned>((n_q - 1) & 1), kTcPollLimit, p.c.err);
@@ -303,9 +328,8 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
         return static_cast<int>((static_cast<long long>(p.c.l0 + w.it.l) * p.c.n_pages + pg) * p.c.nkv + w.it.kh);
       };
       auto fill = [&](const CUtensorMap* map, int t, int z) {
-        const int st = static_cast<int>(n_kv % NS);
-        if (n_kv >= NS)
-          ok = ok && mbar_wait_bounded(&bars.kv_empty[st], static_cast<unsigned>((n_kv / NS - 1) & 1), kTcPollLimit, p.c.err);
+        if (ring_turn > 0)
+          ok = ok && mbar_wait_bounded(&bars.kv_empty[st], (ring_turn - 1) & 1u, kTcPollLimit, p.c.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         if (lane == 0) mbar_arrive_expect_tx(&bars.kv_full[st], P::tile);
@@ -314,6 +338,10 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
           tma_load_3d(smem + P::ring + st * P::tile + box_off, map, my_half * 64, (t * kTcKeys) & (p.c.ps - 1) & ~(prow - 1), z,
                       &bars.kv_full[st]);
         ++n_kv;
+        if (++st == NS) {
+          st = 0;
+          ++ring_turn;
+        }
       };
       const int n = w.t1 - w.t0;
       if (PAIR) {
@@ -339,8 +367,8 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       }
     }
     if (!ok) {  // no copy may land after the CTA has left
-      for (long long i = max(0LL, n_kv - NS); i < n_kv; ++i)
-        mbar_wait_bounded(&bars.kv_full[i % NS], static_cast<unsigned>((i / NS) & 1), kTcPollLimit, p.c.err);
+      for (unsigned i = n_kv > NS ? n_kv - NS : 0u; i < n_kv; ++i)
+        mbar_wait_bounded(&bars.kv_full[i % NS], (i / NS) & 1u, kTcPollLimit, p.c.err);
       if (n_q > 0) mbar_wait_bounded(&bars.q_full, static_cast<unsigned>((n_q - 1) & 1), kTcPollLimit, p.c.err);
     }
   } else if (warp == kTcMmaWarp) {
@@ -349,7 +377,8 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       const uint32_t idesc_qk = umma_idesc_bf16(kTcRows, kTcKeys, false);
       const uint32_t idesc_pv = umma_idesc_bf16(kTcRows, D, true);
       const uint32_t sq = smem_u32(smem + P::q), sr = smem_u32(smem + P::ring);
-      long long n_kv = 0;
+      int ring_st = 0;
+      unsigned ring_turn = 0;
       int n_q = 0;
       unsigned n_p[2] = {0u, 0u};
       auto wait = [&](uint64_t* bar, unsigned parity) {
@@ -359,9 +388,12 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       };
       // takes the ring's next buffer
       auto next_kv = [&](int* st) {
-        *st = static_cast<int>(n_kv % NS);
-        const bool r = wait(&bars.kv_full[*st], static_cast<unsigned>(n_kv / NS));
-        ++n_kv;
+        *st = ring_st;
+        const bool r = wait(&bars.kv_full[ring_st], ring_turn);
+        if (++ring_st == NS) {
+          ring_st = 0;
+          ++ring_turn;
+        }
         return r;
       };
       auto qk = [&](int s, int st) {
@@ -443,7 +475,9 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       }
     }
     __syncwarp();
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcSoftmaxRegs));
     // ---- softmax of stream s, a thread per row
     const int s = warp >> 2, sub = warp & 3;
     const int r = sub * 32 + lane;  // row of the tile, tensor-memory lane
@@ -451,7 +485,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
     const uint32_t t_s = lane_base + static_cast<uint32_t>(s) * kTcKeys;
     const uint32_t t_o = lane_base + 256u + static_cast<uint32_t>(s) * D;
     unsigned n_s = 0, n_piece = 0;
-    long long n_kv = 0;  // ring position of the piece's first buffer
+    unsigned n_kv = 0;  // ring position of the piece's first buffer
     bool wrote = false;
     // after a wait that ran out a warp only keeps the CTA's barriers company
     for (PieceWalk w(run); w.more(); w.next(p)) {
@@ -468,6 +502,21 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
         const int t = w.t0 + i;
         const bool first = i < 2 && (PAIR ? i == 0 : true);
         const bool masked = (t + 1) * kTcKeys > full_end;
+        RowMask vis;
+        if (masked) {
+          vis = row_mask(p, it, node, t);
+          if (!PAIR || s == 0) {
+            // this tile's values: their buffer's place in the loader's order
+            const unsigned at = n_kv + static_cast<unsigned>(PAIR ? 2 * i + 1 : (n == 1 ? 1 : min(2 * i + 2, n + i)));
+            const unsigned st = at % NS;
+            ok = mbar_wait_bounded(&bars.kv_full[st], (at / NS) & 1u, kTcPollLimit, p.c.err);
+            if (!__all_sync(0xffffffffu, ok)) {
+              ok = false;
+              break;
+            }
+            clean_values<D>(smem + P::ring + st * P::tile, full_end - t * kTcKeys, it.kv_end - t * kTcKeys, r, &sh.bad[s]);
+          }
+        }
         ok = mbar_wait_bounded(&bars.s_full[s], n_s & 1u, kTcPollLimit, p.c.err);
         ++n_s;
         if (!__all_sync(0xffffffffu, ok)) {
@@ -475,39 +524,23 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
           break;
         }
         tc_fence_after();
-        if (masked && (!PAIR || s == 0)) {
-          // this tile's values: their buffer's place in the loader's order
-          const long long at = n_kv + (PAIR ? 2 * i + 1 : (n == 1 ? 1 : min(2 * i + 2, n + i)));
-          const int st = static_cast<int>(at % NS);
-          ok = mbar_wait_bounded(&bars.kv_full[st], static_cast<unsigned>((at / NS) & 1), kTcPollLimit, p.c.err);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-          clean_values<D>(smem + P::ring + st * P::tile, it.kv_end - t * kTcKeys, r, &sh.bad[s]);
-        }
         if (warp_live) {
-          // two passes over the scores, 32 columns at a time: the maximum, then
-          // P.  Reading the scores twice keeps a thread within its registers.
-          auto hide = [&](float* x, int c) {
-            if (!masked) return;
-            const uint32_t bits = visible_bits(p, it, node, t * kTcKeys + c);
+          float x[kTcKeys];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!((bits >> j) & 1u)) x[j] = -INFINITY;
-          };
-          float x[2][32];
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          tmem_ld32_async(t_s, x[0]);
+          for (int c = 0; c < kTcKeys; c += 32) tmem_ld32_async(t_s + c, x + c);
+          tmem_ld_wait<kTcKeys>(x);
+          if (masked) {
 #pragma unroll
-          for (int c = 0; c < kTcKeys / 32; ++c) {
-            tmem_ld_wait<32>(x[c & 1]);
-            if (c + 1 < kTcKeys / 32) tmem_ld32_async(t_s + (c + 1) * 32, x[(c + 1) & 1]);
-            hide(x[c & 1], c * 32);
+            for (int c = 0; c < kTcKeys; c += 32) {
+              const uint32_t bits = visible_bits(vis, t, c / 32);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[c & 1][j]);
+              for (int j = 0; j < 32; ++j)
+                if (!((bits >> j) & 1u)) x[c + j] = -INFINITY;
+            }
           }
-          tmem_ld32_async(t_s, x[0]);
+          float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int j = 4; j + 1 < kTcKeys; j += 2) mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], x[j], x[j + 1]);
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
           // the maximum in use may lag behind by 2^8, which fp32 sums and outputs hold easily
           const bool move = top > m + kRescaleLog2 || (m == -INFINITY && top != -INFINITY);
@@ -531,32 +564,28 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
           const float base = m == -INFINITY ? 0.f : m;
           // P is rounded to bf16 for the tensor cores; the sum takes the
           // rounded values, so that the weights still add up to one
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const float2 sc = make_float2(p.scale_log2, p.scale_log2), nb = make_float2(-base, -base);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int c = 0; c < kTcKeys / 32; ++c) {
-            tmem_ld_wait<32>(x[c & 1]);
-            if (c + 1 < kTcKeys / 32) tmem_ld32_async(t_s + (c + 1) * 32, x[(c + 1) & 1]);
-            hide(x[c & 1], c * 32);
-            uint32_t w16[16];
+          for (int c = 0; c < kTcKeys; c += 64) {
+            uint32_t w32[32];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float p0 = exp2_approx(fmaf(x[c & 1][2 * j], p.scale_log2, -base));
-              const float p1 = exp2_approx(fmaf(x[c & 1][2 * j + 1], p.scale_log2, -base));
-              const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
-              w16[j] = *reinterpret_cast<const uint32_t*>(&b);
-              sum[j & 3] += __uint_as_float(w16[j] << 16) + __uint_as_float(w16[j] & 0xffff0000u);
+            for (int j = 0; j < 32; ++j) {
+              const float2 e = fma2(make_float2(x[c + 2 * j], x[c + 2 * j + 1]), sc, nb);
+              const __nv_bfloat162 b = __floats2bfloat162_rn(exp2_approx(e.x), exp2_approx(e.y));
+              w32[j] = *reinterpret_cast<const uint32_t*>(&b);
+              sum[j & 1] = add2(sum[j & 1], make_float2(__uint_as_float(w32[j] << 16), __uint_as_float(w32[j] & 0xffff0000u)));
             }
-            // columns 16 c .. of P lie over scores that are read already
-            tmem_st16(t_s + c * 16, w16);
+            tmem_st32(t_s + c / 2, w32);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           tmem_st_wait();
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.p_full[s]);
       }
-      n_kv += 2LL * n;
+      n_kv += 2u * static_cast<unsigned>(n);
       // ---- result of the piece
       const bool starts = w.t0 == 0, whole = starts && w.t1 == it.nt;
       if (!PAIR) {
@@ -578,11 +607,12 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
           l = a.y * w0 + b.y * w1;
         }
         const int bad = PAIR ? sh.bad[0] : sh.bad[0] | sh.bad[1];
-        const int slot0 = max(w.t0 * kTcKeys, full_end / kTcKeys * kTcKeys);
+        const int slot0 = max(w.t0 * kTcKeys, full_end);
         const int slot1 = min(w.t1 * kTcKeys, it.kv_end);
         const float inv = l == 0.f ? 0.f : 1.0f / l;
         const int g_row = row0 + r, nd = g_row / p.c.G, g = g_row - nd * p.c.G;
         constexpr int NC = PAIR ? D : D / 2;  // columns of this warp group
+        constexpr int W = NC < 64 ? NC : 64;  // columns at a time
         const int c0 = PAIR ? 0 : s * NC;
         const int rr = r + (PAIR ? s * tile_rows : 0);
         const long long slot_row =
@@ -591,33 +621,40 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
           *reinterpret_cast<float2*>(p.part_ml + slot_row * 2) = make_float2(m, l);
         if (warp_live) {
 #pragma unroll 1
-          for (int c = 0; c < NC; c += 32) {
-            float o[32], o1[32];
+          for (int c = 0; c < NC; c += W) {
+            float o[W];
             if (PAIR) {
-              tmem_ld32_async(t_o + c, o);
-              tmem_ld_wait<32>(o);
-            } else {
-              tmem_ld32_async(lane_base + 256u + c0 + c, o);
-              tmem_ld32_async(lane_base + 256u + D + c0 + c, o1);
-              tmem_ld_wait<32>(o);
-              tmem_ld_wait<32>(o1);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = n > 1 ? fmaf(o1[j], w1, o[j] * w0) : o[j] * w0;
+              for (int j = 0; j < W; j += 32) tmem_ld32_async(t_o + c + j, o + j);
+              tmem_ld_wait<W>(o);
+            } else {
+#pragma unroll
+              for (int j = 0; j < W; j += 32) tmem_ld32_async(lane_base + 256u + c0 + c + j, o + j);
+              if (n > 1) {
+                float o1[W];
+#pragma unroll
+                for (int j = 0; j < W; j += 32) tmem_ld32_async(lane_base + 256u + D + c0 + c + j, o1 + j);
+                tmem_ld_wait<W>(o);
+                tmem_ld_wait<W>(o1);
+#pragma unroll
+                for (int j = 0; j < W; ++j) o[j] = fmaf(o1[j], w1, o[j] * w0);
+              } else {
+                tmem_ld_wait<W>(o);
+              }
             }
             if (r < rows) {
-              if (bad) add_nonfinite<32>(p, it, node, slot0, slot1, D, c0 + c, o);
+              if (bad) add_nonfinite<W>(p, it, node, slot0, slot1, D, c0 + c, o);
               if (whole) {
                 __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
                                      (((static_cast<long long>(it.l) * p.c.B + it.b) * p.c.n_max + nd) * p.c.nq +
                                       it.kh * p.c.G + g) * D + c0 + c;
 #pragma unroll
-                for (int j = 0; j < 32; j += 8) {
+                for (int j = 0; j < W; j += 8) {
                   uint32_t u[4];
 #pragma unroll
                   for (int e = 0; e < 4; ++e) {
-                    // a row that sees nothing is zero, whatever P V holds
-                    const float y0 = inv == 0.f ? 0.f : o[j + 2 * e] * inv, y1 = inv == 0.f ? 0.f : o[j + 2 * e + 1] * inv;
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(y0, y1);
+                    // (a row that sees nothing has zeros in O and inv)
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(o[j + 2 * e] * inv, o[j + 2 * e + 1] * inv);
                     u[e] = *reinterpret_cast<const uint32_t*>(&b);
                   }
                   *reinterpret_cast<uint4*>(dst + j) = make_uint4(u[0], u[1], u[2], u[3]);
@@ -625,7 +662,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
               } else {
                 float* dst = p.part_o + slot_row * D + c0 + c;
 #pragma unroll
-                for (int j = 0; j < 32; j += 4)
+                for (int j = 0; j < W; j += 4)
                   *reinterpret_cast<float4*>(dst + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
               }
             }
