@@ -126,7 +126,19 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Two fp32 operations in one instruction, and a maximum of three.
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// Two fp32 operations in one instruction, and a maximum of three (NaN if
+// one of them is).
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;"
@@ -143,8 +155,30 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+
+// P of a row's 128 scores into 64 columns of tensor memory; returns its sum.  P
+// is rounded to bf16 for the tensor cores (off by 2^-9 at most, half a step,
+// as much as the result's own rounding); the sum keeps 32 bits.
+__device__ __forceinline__ float store_probs(float* x, float scale, float base, uint32_t taddr) {
+  const float2 sc = make_float2(scale, scale), nb = make_float2(-base, -base);
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int c = 0; c < kTcKeys; c += 64) {
+    uint32_t w[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float2 e = fma2(make_float2(x[c + 2 * j], x[c + 2 * j + 1]), sc, nb);
+      const float2 y = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+      sum[j & 1] = add2(sum[j & 1], y);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(y.x, y.y);
+      w[j] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    tmem_st32(taddr + c / 2, w);
+  }
+  return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
 // Pieces of a run, the same walk in every role.
@@ -372,17 +406,22 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       if (n_q > 0) mbar_wait_bounded(&bars.q_full, static_cast<unsigned>((n_q - 1) & 1), kTcPollLimit, p.c.err);
     }
   } else if (warp == kTcMmaWarp) {
-    // ---- products, by one thread
-    if (lane == 0) {
+    // ---- products.  The whole warp walks and waits, so that addresses stay
+    // uniform; one elected lane issues.
+    {
+      const bool leader = elect_one();
       const uint32_t idesc_qk = umma_idesc_bf16(kTcRows, kTcKeys, false);
       const uint32_t idesc_pv = umma_idesc_bf16(kTcRows, D, true);
-      const uint32_t sq = smem_u32(smem + P::q), sr = smem_u32(smem + P::ring);
+      const uint64_t d_q = desc_sw128(smem_u32(smem + P::q), 16, 1024);
+      const uint64_t d_k = desc_sw128(smem_u32(smem + P::ring), 16, 1024);
+      const uint64_t d_v = desc_sw128(smem_u32(smem + P::ring), kTcKeys * 128, 1024);
       int ring_st = 0;
       unsigned ring_turn = 0;
       int n_q = 0;
       unsigned n_p[2] = {0u, 0u};
       auto wait = [&](uint64_t* bar, unsigned parity) {
         ok = ok && mbar_wait_bounded(bar, parity & 1u, kTcPollLimit, p.c.err);
+        ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
         return ok;
       };
@@ -396,21 +435,29 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
         }
         return r;
       };
+      auto commit = [&](uint64_t* bar) {
+        if (leader) umma_commit(bar);
+      };
       auto qk = [&](int s, int st) {
+        const uint64_t a = d_q + (PAIR ? s * (P::tile >> 4) : 0), b = d_k + st * (P::tile >> 4);
+        const uint32_t d = tmem + static_cast<uint32_t>(s) * kTcKeys;
+        if (leader) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = static_cast<uint32_t>((k >> 2) * (kTcKeys * 128) + (k & 3) * 32);
-          umma_bf16(tmem + static_cast<uint32_t>(s) * kTcKeys,
-                    desc_sw128(sq + (PAIR ? s * P::tile : 0) + off, 16, 1024),
-                    desc_sw128(sr + st * P::tile + off, 16, 1024), idesc_qk, k > 0);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * (kTcKeys * 128) + (k & 3) * 32) >> 4;
+            umma_bf16(d, a + off, b + off, idesc_qk, k > 0);
+          }
+          umma_commit(&bars.s_full[s]);
         }
-        umma_commit(&bars.s_full[s]);
       };
       auto pv = [&](int s, int st, bool first) {
+        const uint64_t b = d_v + st * (P::tile >> 4);
+        const uint32_t d = tmem + 256u + static_cast<uint32_t>(s) * D, a = tmem + static_cast<uint32_t>(s) * kTcKeys;
+        if (leader) {
 #pragma unroll
-        for (int k = 0; k < kTcKeys / 16; ++k)
-          umma_bf16_ts(tmem + 256u + static_cast<uint32_t>(s) * D, tmem + static_cast<uint32_t>(s) * kTcKeys + k * 8,
-                       desc_sw128(sr + st * P::tile + k * 2048, kTcKeys * 128, 1024), idesc_pv, !(first && k == 0));
+          for (int k = 0; k < kTcKeys / 16; ++k)
+            umma_bf16_ts(d, a + k * 8, b + ((k * 2048) >> 4), idesc_pv, k > 0 || !first);
+        }
       };
       for (PieceWalk w(run); w.more() && ok; w.next(p)) {
         const int n = w.t1 - w.t0;
@@ -421,8 +468,8 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
           if (!next_kv(&st_k)) break;
           qk(0, st_k);
           qk(1, st_k);
-          umma_commit(&bars.kv_empty[st_k]);
-          if (n == 1) umma_commit(&bars.q_empty);
+          commit(&bars.kv_empty[st_k]);
+          if (n == 1) commit(&bars.q_empty);
           for (int i = 0; i < n; ++i) {
             if (!next_kv(&st_v)) break;
             if (!wait(&bars.p_full[0], n_p[0]++)) break;
@@ -431,46 +478,46 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
               if (!next_kv(&st_k)) break;
               qk(0, st_k);
             } else {
-              umma_commit(&bars.o_done[0]);
+              commit(&bars.o_done[0]);
             }
             if (!wait(&bars.p_full[1], n_p[1]++)) break;
             pv(1, st_v, i == 0);
-            umma_commit(&bars.kv_empty[st_v]);
+            commit(&bars.kv_empty[st_v]);
             if (i + 1 < n) {
               qk(1, st_k);
-              umma_commit(&bars.kv_empty[st_k]);
-              if (i + 2 == n) umma_commit(&bars.q_empty);
+              commit(&bars.kv_empty[st_k]);
+              if (i + 2 == n) commit(&bars.q_empty);
             } else {
-              umma_commit(&bars.o_done[1]);
+              commit(&bars.o_done[1]);
             }
           }
         } else {
           for (int i = 0; i < min(n, 2) && ok; ++i) {
             if (!next_kv(&st_k)) break;
             qk(i, st_k);
-            umma_commit(&bars.kv_empty[st_k]);
+            commit(&bars.kv_empty[st_k]);
           }
           if (!ok) break;
-          if (n <= 2) umma_commit(&bars.q_empty);
+          if (n <= 2) commit(&bars.q_empty);
           for (int i = 0; i < n; ++i) {
             const int s = i & 1;
             if (!next_kv(&st_v)) break;
             if (!wait(&bars.p_full[s], n_p[s]++)) break;
             pv(s, st_v, i < 2);
-            umma_commit(&bars.kv_empty[st_v]);
+            commit(&bars.kv_empty[st_v]);
             if (i + 2 < n) {
               if (!next_kv(&st_k)) break;
               qk(s, st_k);
-              umma_commit(&bars.kv_empty[st_k]);
-              if (i + 3 == n) umma_commit(&bars.q_empty);
+              commit(&bars.kv_empty[st_k]);
+              if (i + 3 == n) commit(&bars.q_empty);
             }
           }
-          umma_commit(&bars.o_done[0]);
+          commit(&bars.o_done[0]);
         }
         if (!ok) break;
       }
       if (!ok) {  // products in flight end before tensor memory is freed
-        umma_commit(&bars.drain);
+        if (leader) umma_commit(&bars.drain);
         mbar_wait_bounded(&bars.drain, 0, kTcPollLimit, p.c.err);
       }
     }
@@ -541,9 +588,9 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
           float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
           for (int j = 4; j + 1 < kTcKeys; j += 2) mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], x[j], x[j + 1]);
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+          const float top = max3(mx[0], mx[1], max3(mx[2], mx[3], mx[3])) * p.scale_log2;
           // the maximum in use may lag behind by 2^8, which fp32 sums and outputs hold easily
-          const bool move = top > m + kRescaleLog2 || (m == -INFINITY && top != -INFINITY);
+          const bool move = !(top <= m + kRescaleLog2);  // a NaN score moves it to NaN, and the row with it
           float fix = 1.f;
           if (move) {
             fix = exp2_approx(m - top);
@@ -562,23 +609,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
             }
           }
           const float base = m == -INFINITY ? 0.f : m;
-          // P is rounded to bf16 for the tensor cores; the sum takes the
-          // rounded values, so that the weights still add up to one
-          const float2 sc = make_float2(p.scale_log2, p.scale_log2), nb = make_float2(-base, -base);
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int c = 0; c < kTcKeys; c += 64) {
-            uint32_t w32[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float2 e = fma2(make_float2(x[c + 2 * j], x[c + 2 * j + 1]), sc, nb);
-              const __nv_bfloat162 b = __floats2bfloat162_rn(exp2_approx(e.x), exp2_approx(e.y));
-              w32[j] = *reinterpret_cast<const uint32_t*>(&b);
-              sum[j & 1] = add2(sum[j & 1], make_float2(__uint_as_float(w32[j] << 16), __uint_as_float(w32[j] & 0xffff0000u)));
-            }
-            tmem_st32(t_s + c / 2, w32);
-          }
-          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          l += store_probs(x, p.scale_log2, base, t_s);
           tmem_st_wait();
         }
         tc_fence_before();
