@@ -815,7 +815,7 @@ int sfa_kv_attend(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begi
   // the kernels count key tiles in 32 bits
   const double tiles = static_cast<double>(layer_count) * batch * c->n_kv_heads *
                        ((static_cast<long long>(n_max) * p.c.G + a.rows_step - 1) / a.rows_step) *
-                       ((static_cast<long long>(p.c.max_pages) * p.c.ps + a.kt - 1) / a.kt);
+                       ((static_cast<long long>(p.c.max_pages) * p.c.ps + a.kt - 1) / a.kt + a.item_cost);
   if (tiles > 1073741824.0) return SFA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < a.total) return SFA_ERR_WORKSPACE;
   if (!on_device(h)) return SFA_ERR_INVALID_ARG;
@@ -827,7 +827,8 @@ int sfa_kv_attend(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begi
   p.rows_step = a.rows_step;
   p.kt = a.kt;
   p.n_cta = a.n_cta;
-  p.min_tiles = 1;
+  p.item_cost = a.item_cost;
+  p.spread = kAttendSpread;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(c->head_dim)));
   p.meta = reinterpret_cast<SplitMeta*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + a.off_ml);

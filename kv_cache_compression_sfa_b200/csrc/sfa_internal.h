@@ -257,7 +257,7 @@ struct AttendParams {
   int rows_step;            // rows (node * G + head) of a work item
   int kt;                   // keys of a tile
   int n_cta;                // CTAs that share the tiles
-  int min_tiles;            // fewest tiles of a CTA
+  int item_cost, spread;    // tiles that an item's start and result weigh, from `spread` tiles a CTA on
   float scale_log2;         // log2(e) / sqrt(d)
   SplitMeta* meta;          // [n_cta]
   float* part_ml;           // [n_cta][2][rows_step][2]: running maximum (log2 units), sum
@@ -266,10 +266,15 @@ struct AttendParams {
 
 constexpr int kAttendMaxBatch = 4096;  // sequences of an attend call (prefix sums in shared memory)
 
+#ifndef SFA_SPREAD
+#define SFA_SPREAD 2
+#endif
+constexpr int kAttendSpread = SFA_SPREAD;
+
 // Rows of a work item and keys of a tile of the attend kernels, and the
 // workspace that they need.
 struct AttendPlan {
-  int rows_step, kt, n_cta;
+  int rows_step, kt, n_cta, item_cost;
   size_t off_ml, off_o, total;
 };
 AttendPlan attend_plan(int in_dtype, int head_dim, int G, int n_max, int n_sm);

@@ -44,7 +44,8 @@ __device__ __forceinline__ long long page_base(const PagedParams& c, int l, int 
 // ---- the work of an attend call ---------------------------------------------
 // A work item is (layer, sequence, KV head, row tile): rows_step consecutive
 // rows (node * G + head of the group) against the keys that any of them sees,
-// in tiles of kt.  The tiles of all items, in the order layer, sequence, row
+// in tiles of kt.  An item counts item_cost units for its start and result and
+// one for every tile; the units of all items, in the order layer, sequence, row
 // tile, KV head, are dealt out in equal runs, one to a CTA: a run may end inside
 // an item, whose pieces are then joined by the combine kernel.  Lengths live on
 // the device, so every CTA works out its own run.
@@ -58,11 +59,12 @@ struct AttendItem {
 };
 
 struct AttendRun {
-  AttendItem it;      // item of the first tile
-  int tile;           // its first tile
-  int first;          // global index of the first tile
-  int tiles;          // tiles of this CTA
-  int chunk;          // tiles of every CTA but the last ones
+  AttendItem it;      // item of the first unit
+  int unit;           // which of its units that is
+  int first;          // global index of the first unit
+  int units;          // units of this CTA
+  int chunk;          // units of every CTA but the last ones
+  int cost;           // units that an item counts besides its tiles
 };
 
 __device__ __forceinline__ int row_tiles(const AttendParams& p, int len) {
@@ -134,37 +136,52 @@ __device__ __forceinline__ int seq_tiles_warp(const AttendParams& p, const SeqLe
 
 // This CTA's run, worked out by every calling warp for itself: prefix sums over
 // the sequences by shuffles, so that no warp waits for another.  The host
-// bounds the call's tiles by 2^31.
+// bounds the call's units by 2^31.
 __device__ __forceinline__ AttendRun find_run(const AttendParams& p, bool latch) {
   const int lane = threadIdx.x & 31;
   const int B = p.c.B, nkv = p.c.nkv;
   const bool wide = !p.mask && row_tiles(p, p.c.n_max) > 8;
   const int per = (B + 31) >> 5, b0 = min(B, lane * per), b1 = min(B, b0 + per);
-  int mine = 0, layer;  // tiles of one KV head of this lane's sequences; of all
+  int mine = 0, rows = 0, layer, items;  // tiles and row tiles of one KV head: of this lane's sequences, of all
   if (wide) {
-    layer = 0;
-    for (int b = 0; b < B; ++b) layer += seq_tiles_warp(p, seq_lens(p.c, b, latch && lane == 0), lane);
+    layer = items = 0;
+    for (int b = 0; b < B; ++b) {
+      const SeqLens s = seq_lens(p.c, b, latch && lane == 0);
+      layer += seq_tiles_warp(p, s, lane);
+      items += row_tiles(p, s.len);
+    }
   } else {
-    for (int b = b0; b < b1; ++b) mine += seq_tiles(p, seq_lens(p.c, b, latch));
+    for (int b = b0; b < b1; ++b) {
+      const SeqLens s = seq_lens(p.c, b, latch);
+      mine += seq_tiles(p, s);
+      rows += row_tiles(p, s.len);
+    }
     layer = __reduce_add_sync(0xffffffffu, mine);
+    items = __reduce_add_sync(0xffffffffu, rows);
   }
   AttendRun r;
+  // few tiles: every CTA gets one or two, whatever their items; else an item's
+  // start and result weigh as much as item_cost tiles
+  const int c = layer * nkv * p.c.Lc <= p.spread * p.n_cta ? 0 : p.item_cost;
+  r.cost = c;
+  layer += c * items;
+  mine += c * rows;
   const int total = layer * nkv * p.c.Lc;
-  r.chunk = max(p.min_tiles, (total + p.n_cta - 1) / p.n_cta);
+  r.chunk = max(1, (total + p.n_cta - 1) / p.n_cta);
   const long long first = static_cast<long long>(blockIdx.x) * r.chunk;
   r.first = static_cast<int>(min(first, static_cast<long long>(total)));
-  r.tiles = min(r.chunk, total - r.first);
-  r.tile = 0;
-  if (r.tiles <= 0) return r;
+  r.units = min(r.chunk, total - r.first);
+  r.unit = 0;
+  if (r.units <= 0) return r;
   const int l = r.first / (layer * nkv);
-  int rem = r.first - l * layer * nkv;  // tile within the layer
+  int rem = r.first - l * layer * nkv;  // unit within the layer
   // the sequence: prefix sums count one KV head, the order within a sequence is row tile, KV head
   SeqLens s;
   int b = 0;
   if (wide) {
     for (;; ++b) {
       s = seq_lens(p.c, b, false);
-      const int n = seq_tiles_warp(p, s, lane) * nkv;
+      const int n = (seq_tiles_warp(p, s, lane) + c * row_tiles(p, s.len)) * nkv;
       if (rem < n) break;
       rem -= n;
     }
@@ -176,7 +193,7 @@ __device__ __forceinline__ AttendRun find_run(const AttendParams& p, bool latch)
     if (per > 1) {
       for (;; ++b) {
         s = seq_lens(p.c, b, false);
-        const int n = seq_tiles(p, s) * nkv;
+        const int n = (seq_tiles(p, s) + c * row_tiles(p, s.len)) * nkv;
         if (rem < n) break;
         rem -= n;
       }
@@ -189,14 +206,14 @@ __device__ __forceinline__ AttendRun find_run(const AttendParams& p, bool latch)
   r.it.ctx = s.ctx;
   r.it.len = s.len;
   const int nrt = row_tiles(p, s.len);
-  int rt = 0, nt = 0;
+  int rt = 0, nt = 0;  // nt: units of the row tile
   if (p.mask) {
-    nt = (s.ctx + s.len + p.kt - 1) / p.kt;
+    nt = (s.ctx + s.len + p.kt - 1) / p.kt + c;
     rt = rem / (nt * nkv);
     rem -= rt * nt * nkv;
   } else {
     for (int base = 0; base < nrt; base += 32) {  // the row tile that holds the remainder, 32 at a time
-      const int t = base + lane < nrt ? tiles_of(p, s.ctx, s.len, base + lane) : 0;
+      const int t = base + lane < nrt ? tiles_of(p, s.ctx, s.len, base + lane) + c : 0;
       const int inc = warp_scan(t, lane) * nkv;
       const unsigned hit = __ballot_sync(0xffffffffu, inc > rem);
       if (hit) {
@@ -211,10 +228,36 @@ __device__ __forceinline__ AttendRun find_run(const AttendParams& p, bool latch)
   }
   r.it.rt = rt;
   r.it.kh = rem / nt;
-  r.tile = rem - r.it.kh * nt;
+  r.unit = rem - r.it.kh * nt;
   set_item(p, r.it);
   return r;
 }
+
+// Pieces of a run, the same walk in every role: tiles t0 .. t1 - 1 of item `it`.
+struct PieceWalk {
+  AttendItem it;
+  int t0, t1, unit, left, cost;  // unit: which of the item's units comes first; left: units of the run from there on
+  __device__ __forceinline__ explicit PieceWalk(const AttendRun& r) : it(r.it), unit(r.unit), left(r.units), cost(r.cost) {
+    if (left > 0) cut();
+  }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ void next(const AttendParams& p) {
+    left -= cost + it.nt - unit;
+    if (left <= 0) return;
+    next_item(p, it);
+    unit = 0;
+    cut();
+  }
+  // global index of the item's first unit
+  __device__ __forceinline__ int item_first(const AttendRun& r) const { return r.first + r.units - left - unit; }
+
+ private:
+  __device__ __forceinline__ void cut() {
+    t0 = max(0, unit - cost);
+    t1 = min(it.nt, unit + left - cost);
+    if (t1 <= t0) left = 0;  // the run ends before the item's first tile, which the next CTA's takes
+  }
+};
 
 // Partial result slot of a piece: a CTA has at most one piece that continues an
 // item and one that starts an item without finishing it.
@@ -226,7 +269,7 @@ __device__ __forceinline__ void write_meta(const AttendParams& p, const AttendRu
   SplitMeta m = {};
   m.last_cta = -1;
   if (starts_split) {
-    m.last_cta = (item_first + it.nt - 1) / r.chunk;
+    m.last_cta = (item_first + r.cost + it.nt - 1) / r.chunk;
     m.l = it.l;
     m.b = it.b;
     m.kh = it.kh;

@@ -9,6 +9,9 @@
 namespace sfa {
 namespace {
 
+#ifndef SFA_ITEM_COST
+#define SFA_ITEM_COST 4
+#endif
 constexpr int kSimtThreads = 256;
 constexpr int kSimtWarps = kSimtThreads / 32;
 constexpr int kSimtKeys = 64;  // keys of a tile
@@ -75,12 +78,10 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attend_simt_kernel(const __gr
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float* s_q = reinterpret_cast<float*>(smem + P::q);
   float* s_p = reinterpret_cast<float*>(smem + P::pr) + warp * kSimtKeys * RPW;
-  AttendItem it = run.it;
-  int left = run.tiles;
-  int t0 = run.tile;
   bool wrote = false;
-  while (left > 0) {
-    const int t1 = min(it.nt, t0 + left);
+  for (PieceWalk w(run); w.more(); w.next(p)) {
+    const AttendItem& it = w.it;
+    const int t0 = w.t0, t1 = w.t1;
     // q of the item's rows, scaled to log2 units
     for (int a = tid; a < P::R * (D / 4); a += kSimtThreads) {
       const int r = a / (D / 4), d4 = (a - r * (D / 4)) * 4;
@@ -190,15 +191,12 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attend_simt_kernel(const __gr
       }
     }
     if (starts && !whole) {
-      if (tid == 0) write_meta(p, run, true, it, run.first + run.tiles - left);
+      if (tid == 0) write_meta(p, run, true, it, w.item_first(run));
       wrote = true;
     }
-    left -= t1 - t0;
-    t0 = 0;
-    if (left > 0) next_item(p, it);
     __syncthreads();  // q and the stages are reused
   }
-  if (!wrote && tid == 0) write_meta(p, run, false, it, 0);
+  if (!wrote && tid == 0) write_meta(p, run, false, run.it, 0);
 }
 
 // Joins the pieces of split items: a warp per row, in the order of the pieces,
@@ -309,6 +307,7 @@ AttendPlan attend_plan(int in_dtype, int head_dim, int G, int n_max, int n_sm) {
     attend_tc_rows(G, n_max, &a.rows_step, &a.kt);
   }
   a.n_cta = n_sm;
+  a.item_cost = in_dtype == SFA_F32 ? 2 : SFA_ITEM_COST;
   a.off_ml = static_cast<size_t>(align256(static_cast<long long>(sizeof(SplitMeta)) * a.n_cta));
   a.off_o = a.off_ml + static_cast<size_t>(align256(16LL * a.n_cta * a.rows_step));
   a.total = a.off_o + static_cast<size_t>(align256(8LL * a.n_cta * a.rows_step * head_dim));

@@ -58,7 +58,7 @@ struct TcMaps {
 };
 
 struct TcBars {
-  uint64_t q_full, q_empty;
+  uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[12], kv_empty[12];
   uint64_t s_full[2], p_full[2], o_done[2], drain;
 };
@@ -181,23 +181,6 @@ __device__ __forceinline__ float store_probs(float* x, float scale, float base, 
   return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
-// Pieces of a run, the same walk in every role.
-struct PieceWalk {
-  AttendItem it;
-  int t0, t1, left;
-  __device__ __forceinline__ explicit PieceWalk(const AttendRun& r) : it(r.it), t0(r.tile), t1(0), left(r.tiles) {
-    if (left > 0) t1 = min(it.nt, t0 + left);
-  }
-  __device__ __forceinline__ bool more() const { return left > 0; }
-  __device__ __forceinline__ void next(const AttendParams& p) {
-    left -= t1 - t0;
-    if (left <= 0) return;
-    next_item(p, it);
-    t0 = 0;
-    t1 = min(it.nt, left);
-  }
-};
-
 // Visibility of tile t's keys to one row: keys below `end`, and of the new
 // tokens those of the row's mask words (tree).  The words are loaded before
 // the scores are waited for.
@@ -293,8 +276,10 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
   TcBars& bars = sh.bars;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
-    mbar_init(&bars.q_full, 1);
-    mbar_init(&bars.q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.q_full[i], 1);
+      mbar_init(&bars.q_empty[i], 1);
+    }
     for (int i = 0; i < NS; ++i) {
       mbar_init(&bars.kv_full[i], 1);
       mbar_init(&bars.kv_empty[i], 1);
@@ -316,6 +301,8 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
   pdl_wait();
   const AttendRun run = find_run(p, blockIdx.x == 0 && warp == 0);
   const uint32_t tmem = sh.tmem;
+  // up to 64 rows leave room for the next item's q behind this one's
+  const int q_bufs = !PAIR && p.rows_step <= kTcRows / 2 ? 2 : 1;
   const int tile_rows = PAIR ? p.rows_step / 2 : p.rows_step;  // rows of one row tile
   bool ok = true;
 
@@ -334,20 +321,6 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
     unsigned n_kv = 0, st = 0, ring_turn = 0;  // buffers filled so far; the next one and its turn
     int n_q = 0;
     for (PieceWalk w(run); w.more() && ok; w.next(p)) {
-      if (n_q > 0) ok = mbar_wait_bounded(&bars.q_empty, static_cast<unsigned>((n_q - 1) & 1), kTcPollLimit, p.c.err);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const int node0 = w.it.row0 / p.c.G;
-      const int nb = tile_rows / p.c.G;
-      if (lane == 0) {
-        const unsigned qbytes = static_cast<unsigned>(tile_rows * 128 * (D / 64) * (PAIR ? 2 : 1));
-        mbar_arrive_expect_tx(&bars.q_full, qbytes);
-        for (int s = 0; s < (PAIR ? 2 : 1); ++s)
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_4d(smem + P::q + s * P::tile + h * (kTcRows * 128), &maps.q, h * 64, w.it.kh * p.c.G,
-                        node0 + s * nb, w.it.l * p.c.B + w.it.b, &bars.q_full);
-      }
-      ++n_q;
       const int* table = p.c.table + static_cast<long long>(w.it.b) * p.c.max_pages;
       const int slot_end = w.it.kv_end;
       // z coordinate (page and head) of this lane's box in tile t; a box without a key reads as zeros
@@ -377,12 +350,32 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
           ++ring_turn;
         }
       };
+      // q goes behind the item's first keys: its buffer may still be in use
+      auto load_q = [&]() {
+        const int qb = n_q % q_bufs, turn = n_q / q_bufs;
+        if (turn > 0)
+          ok = ok && mbar_wait_bounded(&bars.q_empty[qb], static_cast<unsigned>((turn - 1) & 1), kTcPollLimit, p.c.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        const int node0 = w.it.row0 / p.c.G;
+        const int nb = tile_rows / p.c.G;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars.q_full[qb], static_cast<unsigned>(tile_rows * 128 * (D / 64) * (PAIR ? 2 : 1)));
+          for (int s = 0; s < (PAIR ? 2 : 1); ++s)
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_4d(smem + P::q + s * P::tile + qb * (kTcRows / 2 * 128) + h * (kTcRows * 128), &maps.q, h * 64,
+                          w.it.kh * p.c.G, node0 + s * nb, w.it.l * p.c.B + w.it.b, &bars.q_full[qb]);
+        }
+        __syncwarp();
+        ++n_q;
+      };
       const int n = w.t1 - w.t0;
       if (PAIR) {
         int z = coord(w.t0);
         for (int i = 0; i < n && ok; ++i) {
           const int zn = coord(w.t0 + i + 1);
           fill(&maps.k, w.t0 + i, z);
+          if (i == 0 && ok) load_q();
           if (ok) fill(&maps.v, w.t0 + i, z);
           z = zn;
         }
@@ -390,6 +383,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
         int z0 = coord(w.t0), z1 = coord(w.t0 + 1), z2 = coord(w.t0 + 2);
         fill(&maps.k, w.t0, z0);
         if (n > 1 && ok) fill(&maps.k, w.t0 + 1, z1);
+        if (ok) load_q();
         for (int i = 0; i < n && ok; ++i) {
           const int z3 = coord(w.t0 + i + 3);
           fill(&maps.v, w.t0 + i, z0);
@@ -403,7 +397,8 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
     if (!ok) {  // no copy may land after the CTA has left
       for (unsigned i = n_kv > NS ? n_kv - NS : 0u; i < n_kv; ++i)
         mbar_wait_bounded(&bars.kv_full[i % NS], (i / NS) & 1u, kTcPollLimit, p.c.err);
-      if (n_q > 0) mbar_wait_bounded(&bars.q_full, static_cast<unsigned>((n_q - 1) & 1), kTcPollLimit, p.c.err);
+      for (int i = max(0, n_q - q_bufs); i < n_q; ++i)
+        mbar_wait_bounded(&bars.q_full[i % q_bufs], static_cast<unsigned>((i / q_bufs) & 1), kTcPollLimit, p.c.err);
     }
   } else if (warp == kTcMmaWarp) {
     // ---- products.  The whole warp walks and waits, so that addresses stay
@@ -438,8 +433,8 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       auto commit = [&](uint64_t* bar) {
         if (leader) umma_commit(bar);
       };
-      auto qk = [&](int s, int st) {
-        const uint64_t a = d_q + (PAIR ? s * (P::tile >> 4) : 0), b = d_k + st * (P::tile >> 4);
+      auto qk = [&](int s, int st, uint64_t q_desc) {
+        const uint64_t a = q_desc + (PAIR ? s * (P::tile >> 4) : 0), b = d_k + st * (P::tile >> 4);
         const uint32_t d = tmem + static_cast<uint32_t>(s) * kTcKeys;
         if (leader) {
 #pragma unroll
@@ -461,22 +456,24 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       };
       for (PieceWalk w(run); w.more() && ok; w.next(p)) {
         const int n = w.t1 - w.t0;
-        if (!wait(&bars.q_full, static_cast<unsigned>(n_q))) break;
+        const int qb = n_q % q_bufs;
+        if (!wait(&bars.q_full[qb], static_cast<unsigned>(n_q / q_bufs))) break;
         ++n_q;
+        const uint64_t d_qb = d_q + (qb * (kTcRows / 2 * 128) >> 4);
         int st_k, st_v;
         if (PAIR) {
           if (!next_kv(&st_k)) break;
-          qk(0, st_k);
-          qk(1, st_k);
+          qk(0, st_k, d_qb);
+          qk(1, st_k, d_qb);
           commit(&bars.kv_empty[st_k]);
-          if (n == 1) commit(&bars.q_empty);
+          if (n == 1) commit(&bars.q_empty[qb]);
           for (int i = 0; i < n; ++i) {
             if (!next_kv(&st_v)) break;
             if (!wait(&bars.p_full[0], n_p[0]++)) break;
             pv(0, st_v, i == 0);
             if (i + 1 < n) {
               if (!next_kv(&st_k)) break;
-              qk(0, st_k);
+              qk(0, st_k, d_qb);
             } else {
               commit(&bars.o_done[0]);
             }
@@ -484,9 +481,9 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
             pv(1, st_v, i == 0);
             commit(&bars.kv_empty[st_v]);
             if (i + 1 < n) {
-              qk(1, st_k);
+              qk(1, st_k, d_qb);
               commit(&bars.kv_empty[st_k]);
-              if (i + 2 == n) commit(&bars.q_empty);
+              if (i + 2 == n) commit(&bars.q_empty[qb]);
             } else {
               commit(&bars.o_done[1]);
             }
@@ -494,11 +491,11 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
         } else {
           for (int i = 0; i < min(n, 2) && ok; ++i) {
             if (!next_kv(&st_k)) break;
-            qk(i, st_k);
+            qk(i, st_k, d_qb);
             commit(&bars.kv_empty[st_k]);
           }
           if (!ok) break;
-          if (n <= 2) commit(&bars.q_empty);
+          if (n <= 2) commit(&bars.q_empty[qb]);
           for (int i = 0; i < n; ++i) {
             const int s = i & 1;
             if (!next_kv(&st_v)) break;
@@ -507,9 +504,9 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
             commit(&bars.kv_empty[st_v]);
             if (i + 2 < n) {
               if (!next_kv(&st_k)) break;
-              qk(s, st_k);
+              qk(s, st_k, d_qb);
               commit(&bars.kv_empty[st_k]);
-              if (i + 3 == n) commit(&bars.q_empty);
+              if (i + 3 == n) commit(&bars.q_empty[qb]);
             }
           }
           commit(&bars.o_done[0]);
@@ -700,7 +697,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
           }
         }
         if (starts && !whole) {
-          if (tid == 0) write_meta(p, run, true, it, run.first + run.tiles - w.left);
+          if (tid == 0) write_meta(p, run, true, it, w.item_first(run));
           wrote = true;
         }
         tc_fence_before();
