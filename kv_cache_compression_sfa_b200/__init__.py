@@ -601,6 +601,16 @@ class SfaOperator:
 # ------------------------------------------------------ paged key/value cache
 
 
+try:  # the per-step calls without ctypes; the Python checks below serve where it is not built
+    from . import _fast
+except ImportError:
+    _fast = None
+
+
+def _address(fn) -> int:
+    return ctypes.cast(fn, ctypes.c_void_p).value
+
+
 class SfaRope:
     """Position rotation of sfa_kv_append (``sfa_rope``): the first ``dims``
     elements of a head (0: all), in ``style`` SFA_ROPE_HALF or SFA_ROPE_PAIRS,
@@ -616,6 +626,7 @@ class SfaRope:
                      else (ctypes.c_double * len(self.inv_freq))(*self.inv_freq))
         self.c = sfa_rope(self.style, self.dims, self.base, self._arr)
         self.ref = ctypes.byref(self.c)
+        self.address = ctypes.addressof(self.c)
 
     def check(self, head_dim: int) -> None:
         if self.inv_freq is None:
@@ -657,6 +668,13 @@ def sfa_tree_plan(h: Handle, parents: torch.Tensor, ctx_lens: torch.Tensor,
     if not isinstance(parents, torch.Tensor) or parents.dim() != 2:
         raise ValueError("parents must be a [batch, n] tensor")
     B, n = parents.shape
+    if _fast is not None and positions is not None and mask is not None and parents.is_cuda:
+        rc = _fast.plan(_plan_address(), h.ptr, parents, ctx_lens, lens, positions, mask,
+                        None if stream is None else _stream_ptr(stream))
+        if rc == SFA_OK:
+            return positions, mask
+        if rc is not None:
+            raise SfaError(rc, "sfa_tree_plan")
     dev, i32 = parents.get_device(), torch.int32
     words = (n + 31) // 32
     if positions is None:
@@ -672,6 +690,16 @@ def sfa_tree_plan(h: Handle, parents: torch.Tensor, ctx_lens: torch.Tensor,
     if rc != SFA_OK:
         raise SfaError(rc, "sfa_tree_plan")
     return positions, mask
+
+
+_plan_addr = None
+
+
+def _plan_address() -> int:
+    global _plan_addr
+    if _plan_addr is None:
+        _plan_addr = _address(load_library().sfa_tree_plan)
+    return _plan_addr
 
 
 def _zeros_for(shape, dtype, device, stream):
@@ -723,6 +751,11 @@ class SfaPagedCache:
         self._q_tail, self._kv_tail = (c.n_q_heads, c.head_dim), (c.n_kv_heads, c.head_dim)
         lib = load_library()
         self._append_fn, self._attend_fn, self._accept_fn = lib.sfa_kv_append, lib.sfa_kv_attend, lib.sfa_kv_accept
+        self._spec = None
+        if _fast is not None and dev >= 0:
+            self._spec = _fast.spec(_address(lib.sfa_kv_append), _address(lib.sfa_kv_attend), _address(lib.sfa_kv_accept),
+                                    ctypes.addressof(self.c), dev, c.in_dtype == SFA_BF16, self.batch, *self._q_tail[:1],
+                                    *self._kv_tail)
 
     def _len_ptr(self, t, name: str) -> Optional[int]:
         return None if t is None else _need(t, name, torch.int32, self._lens_shape, self._index)
@@ -751,6 +784,16 @@ class SfaPagedCache:
         """Rotated keys and values of the new tokens into their pages; returns
         (q_out, k_out), the rotated queries (a new tensor unless given; None
         without q) and keys (None unless given)."""
+        if self._spec is not None and (q is None or q_out is not None):
+            if rope is not None:
+                rope.check(self._kv_tail[1])
+            rc = _fast.append(self._spec, self.handle.ptr, layer_begin, q, k, v, ctx_lens, lens, positions,
+                              None if rope is None else rope.address, q_out, k_out,
+                              None if stream is None else _stream_ptr(stream))
+            if rc == SFA_OK:
+                return q_out, k_out
+            if rc is not None:
+                raise SfaError(rc, "sfa_kv_append")
         if k.dim() != 5:
             raise ValueError("k must be [layers, batch, n, n_kv, d]")
         dev, dt, B = self._index, self._dtype, self.batch
@@ -788,6 +831,14 @@ class SfaPagedCache:
         out [layers, B, n, hidden] in the input dtype.  mask [B, n, words] as of
         sfa_tree_plan, or None: every new token sees those before it.  Rows past
         lens keep what out held (a new out is zero there)."""
+        if self._spec is not None and out is not None and q.dim() == 5 and q.shape[2] > 0:
+            rc = _fast.attend(self._spec, self.handle.ptr, layer_begin, q, ctx_lens, lens, mask, out,
+                              self._workspace(q.shape[2], stream) if workspace is None else workspace,
+                              None if stream is None else _stream_ptr(stream))
+            if rc == SFA_OK:
+                return out
+            if rc is not None:
+                raise SfaError(rc, "sfa_kv_attend")
         if q.dim() != 5:
             raise ValueError("q must be [layers, batch, n, n_q, d]")
         dev, dt, B = self._index, self._dtype, self.batch
@@ -817,6 +868,13 @@ class SfaPagedCache:
         """The keys and values of nodes path[b, :n_accept[b]] ([B, n] and [B]
         int32, rising node indices) moved up behind the context; the caller
         then adds n_accept to ctx_lens."""
+        if self._spec is not None:
+            rc = _fast.accept(self._spec, self.handle.ptr, layer_begin, layer_count, path, n_accept, ctx_lens,
+                              None if stream is None else _stream_ptr(stream))
+            if rc == SFA_OK:
+                return
+            if rc is not None:
+                raise SfaError(rc, "sfa_kv_accept")
         if path.dim() != 2:
             raise ValueError("path must be [batch, n]")
         dev, B, n = self._index, self.batch, path.shape[1]

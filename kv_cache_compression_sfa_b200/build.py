@@ -17,6 +17,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsfa.so")
+FAST_SRC = os.path.join(CSRC, "binding_fast.cpp")
+FAST_LIB = os.path.join(PKG, "_fast.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -68,6 +70,33 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     return LIB
 
 
+def build_fast(force: bool = False, verbose: bool = False) -> str:
+    """The Python extension of the per-step paged cache calls, against torch's
+    headers (host code only).  The binding works without it, slower."""
+    deps = (FAST_SRC, os.path.join(INCLUDE, "sfa.h"), os.path.abspath(__file__))
+    if not force and os.path.exists(FAST_LIB) and all(os.path.getmtime(d) <= os.path.getmtime(FAST_LIB) for d in deps):
+        return FAST_LIB
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    inc = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], INCLUDE,
+                                           os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    tmp = FAST_LIB + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-isystem{d}" for d in inc], FAST_SRC, "-o", tmp,
+           # torch's own libraries, loaded by the time the module is
+           *[f"-L{d}" for d in cpp_extension.library_paths()],
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, FAST_LIB)
+    return FAST_LIB
+
+
 if __name__ == "__main__":
     build(force="--force" in sys.argv, verbose=True, ptxas_info="--ptxas" in sys.argv)
+    build_fast(force="--force" in sys.argv, verbose=True)
     print(LIB)
