@@ -786,7 +786,7 @@ int sfa_kv_append(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begi
   p.q_out = q_out;
   p.k_out = k_out;
   p.positions = positions;
-  return cuda_status(launch_kv_append(p, h->cfg.in_dtype, h->cfg.head_dim, h->n_sm, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_kv_append(p, h->cfg.in_dtype, h->cfg.head_dim, static_cast<cudaStream_t>(stream)));
 }
 
 size_t sfa_kv_attend_workspace_bytes(const sfa_handle* h, int n_max) {

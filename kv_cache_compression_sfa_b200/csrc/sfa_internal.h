@@ -219,7 +219,6 @@ struct AppendParams {
   void* k_out;              // may be null, or k
   const int* positions;     // [B][n_max], or null: ctx + i
   int style, dims;          // sfa_rope; dims = 0: no rotation
-  int tokens_per_cta;
   double turns[kMaxRopePairs];  // f_j / (2 pi): turns per position
 };
 
@@ -280,7 +279,7 @@ struct AttendPlan {
 AttendPlan attend_plan(int in_dtype, int head_dim, int G, int n_max, int n_sm);
 
 cudaError_t launch_tree_plan(const PlanParams& p, cudaStream_t s);
-cudaError_t launch_kv_append(const AppendParams& p, int in_dtype, int head_dim, int n_sm, cudaStream_t s);
+cudaError_t launch_kv_append(const AppendParams& p, int in_dtype, int head_dim, cudaStream_t s);
 cudaError_t launch_kv_accept(const AcceptParams& p, int in_dtype, int head_dim, cudaStream_t s);
 cudaError_t launch_kv_attend(const AttendParams& p, int in_dtype, int head_dim, cudaStream_t s);
 cudaError_t attend_prepare(int device);

@@ -2,16 +2,14 @@
 // positions of drafted trees, append with rotation, and the accepted path.
 #include <cuda_runtime.h>
 
-#include <algorithm>
-
 #include "sfa_paged.cuh"
 
 namespace sfa {
 namespace {
 
 constexpr int kPlanThreads = 128;
-constexpr int kAppendThreads = 256;
-constexpr int kAppendMaxTokens = 8;
+constexpr int kAppendThreads = 128;
+constexpr int kAppendAhead = 3;  // rows of a lane in flight
 constexpr int kAcceptThreads = 128;
 constexpr int kAcceptBatch = 8;
 
@@ -88,123 +86,120 @@ __device__ __forceinline__ void unpack16(const uint4& r, float* f) {
   Load16<T>::run(reinterpret_cast<const T*>(&r), f);
 }
 
-// Tokens of the call in runs of tokens_per_cta; a task is one pair of 16-byte
-// chunks of one head of one token: q heads, then keys, then values.  The
-// angles of a token are computed once for its n_q + n_kv heads: turns p * f_j
-// in 64 bits less their whole part, then sine and cosine of the rest in fp32.
+// A warp per token.  A task is a pair of 16-byte chunks of one head row (q heads,
+// then keys, then values): TPH neighbouring lanes share a row, so that accesses
+// are whole 128-byte lines, and a lane keeps its chunks and steps over the rows,
+// kAppendAhead of them loaded before the first is used.  The token's angles are
+// computed once, D / 64 of them by a lane, and handed round by shuffles: turns
+// p * f_j in 64 bits less their whole part, then sine and cosine of the rest in
+// fp32.  Nothing is shared between warps, so that the other warps of the SM
+// cover the chain from the lengths over the page table to the stores (65,536
+// tokens of 28 + 4 + 4 heads of 128, half of them past their sequence's length:
+// 72 us, 6.0 TB/s; tokens in groups of 8 that share their angles in shared
+// memory took 121 us).
 template <typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int V = 16 / static_cast<int>(sizeof(T));  // elements of a chunk
-  constexpr int TPH = D / (2 * V);                     // tasks of a head
-  __shared__ float2 s_cs[kAppendMaxTokens][D / 2];
-  __shared__ long long s_dst[kAppendMaxTokens];        // row offset in kv head 0 of the page; -1: not written
-  __shared__ int s_live[kAppendMaxTokens];
+  constexpr int TPH = D / (2 * V);                     // lanes of a row
+  constexpr int RPW = 32 / TPH;                        // rows of one pass
+  constexpr int NA = D / 64;                           // angles of a lane
   const PagedParams& c = p.c;
+  const int lane = threadIdx.x & 31;
+  const long long t = static_cast<long long>(blockIdx.x) * (kAppendThreads / 32) + (threadIdx.x >> 5);
   pdl_trigger();
   pdl_wait();
-  const long long total = static_cast<long long>(c.Lc) * c.B * c.n_max;
-  const long long t0 = static_cast<long long>(blockIdx.x) * p.tokens_per_cta;
-  const int nt = static_cast<int>(min(static_cast<long long>(p.tokens_per_cta), total - t0));
-  if (static_cast<int>(threadIdx.x) < nt) {
-    const long long t = t0 + threadIdx.x;
-    const int i = static_cast<int>(t % c.n_max);
-    const long long lb = t / c.n_max;
-    const int b = static_cast<int>(lb % c.B), l = static_cast<int>(lb / c.B);
-    const SeqLens sl = seq_lens(c, b, i == 0);
-    s_live[threadIdx.x] = i < sl.len;
-    if (i < sl.len) {
-      const int slot = sl.ctx + i;
-      const int pg = page_of(c, b, slot);
-      s_dst[threadIdx.x] = pg < 0 ? -1 : page_base<D>(c, c.l0 + l, pg, 0) + static_cast<long long>(slot & (c.ps - 1)) * D;
+  if (t >= static_cast<long long>(c.Lc) * c.B * c.n_max) return;
+  const int lb = static_cast<int>(t / c.n_max), i = static_cast<int>(t - static_cast<long long>(lb) * c.n_max);
+  const int l = lb / c.B, b = lb - l * c.B;
+  const SeqLens sl = seq_lens(c, b, i == 0 && lane == 0);
+  if (i >= sl.len) return;
+  const int slot = sl.ctx + i;
+  const int pg = page_of(c, b, slot, lane == 0);
+  const long long dst = page_base<D>(c, c.l0 + l, max(pg, 0), 0) + static_cast<long long>(slot & (c.ps - 1)) * D;
+
+  const int rc = p.dims / V;  // chunks of a row that are rotated
+  // the two chunks of this lane: a rotated pair of halves, or neighbours
+  const int ch = lane % TPH;
+  const bool halves = p.style == SFA_ROPE_HALF && ch < rc / 2;
+  const int c0 = halves ? ch : 2 * ch, c1 = halves ? ch + rc / 2 : 2 * ch + 1;
+  const bool turns_here = c0 < rc;
+  float co[V], si[V];  // of this lane's V pairs
+  if (p.dims > 0) {
+    const int pos = p.positions ? p.positions[static_cast<long long>(b) * c.n_max + i] : slot;
+    float mc[NA], ms[NA];
+#pragma unroll
+    for (int a = 0; a < NA; ++a) {
+      const double turns = static_cast<double>(pos) * p.turns[lane * NA + a];  // zero past dims / 2
+      sincospif(2.0f * static_cast<float>(turns - rint(turns)), &ms[a], &mc[a]);
+    }
+    const int first = p.style == SFA_ROPE_HALF ? c0 * V : c0 * V / 2;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const int j = first + e;
+      co[e] = __shfl_sync(0xffffffffu, mc[e % NA], j / NA);
+      si[e] = __shfl_sync(0xffffffffu, ms[e % NA], j / NA);
     }
   }
-  const int half = p.dims / 2;
-  for (int a = threadIdx.x; a < nt * half; a += kAppendThreads) {
-    const int tt = a / half, j = a - tt * half;
-    const long long t = t0 + tt;
-    const long long lb = t / c.n_max;
-    const int b = static_cast<int>(lb % c.B), i = static_cast<int>(t - lb * c.n_max);
-    const int pos = p.positions ? p.positions[static_cast<long long>(b) * c.n_max + i] : c.ctx[b] + i;
-    const double turns = static_cast<double>(pos) * p.turns[j];
-    float s, co;
-    sincospif(2.0f * static_cast<float>(turns - rint(turns)), &s, &co);
-    s_cs[tt][j] = make_float2(co, s);
-  }
-  __syncthreads();
-  const int heads = (p.q ? c.nq : 0) + 2 * c.nkv;
-  const int qh = p.q ? c.nq : 0;
-  const int tasks = nt * heads * TPH;
-  const int rc = p.dims / V;  // chunks of a head that are rotated
-  for (int a = threadIdx.x; a < tasks; a += kAppendThreads) {
-    const int th = a / TPH, ch = a - th * TPH;
-    const int tt = th / heads, head = th - tt * heads;
-    if (!s_live[tt]) continue;
-    const long long t = t0 + tt;
-    const T* src;
-    T* dst0 = nullptr;  // token-major output
-    T* dst1 = nullptr;  // page
-    const long long pg = s_dst[tt];
-    bool rot = true;
-    if (head < qh) {
-      const long long off = (t * c.nq + head) * D;
-      src = static_cast<const T*>(p.q) + off;
-      dst0 = static_cast<T*>(p.q_out) + off;
-    } else if (head < qh + c.nkv) {
-      const int kh = head - qh;
-      const long long off = (t * c.nkv + kh) * D;
-      src = static_cast<const T*>(p.k) + off;
-      if (p.k_out) dst0 = static_cast<T*>(p.k_out) + off;
-      if (pg >= 0) dst1 = static_cast<T*>(c.k_pages) + pg + static_cast<long long>(kh) * c.ps * D;
-    } else {
-      const int kh = head - qh - c.nkv;
-      src = static_cast<const T*>(p.v) + (t * c.nkv + kh) * D;
-      if (pg >= 0) dst1 = static_cast<T*>(c.v_pages) + pg + static_cast<long long>(kh) * c.ps * D;
-      rot = false;
-    }
-    // the two chunks of this task: a rotated pair of halves, or neighbours
-    int c0, c1;
-    if (p.style == SFA_ROPE_HALF && ch < rc / 2) {
-      c0 = ch;
-      c1 = ch + rc / 2;
-    } else {
-      c0 = 2 * ch;
-      c1 = c0 + 1;
-    }
-    uint4 x0 = *reinterpret_cast<const uint4*>(src + c0 * V);
-    uint4 x1 = *reinterpret_cast<const uint4*>(src + c1 * V);
-    if (rot && c0 < rc) {
-      float f0[V], f1[V];
-      unpack16<T>(x0, f0);
-      unpack16<T>(x1, f1);
-      if (p.style == SFA_ROPE_HALF) {
+  const int qh = p.q ? c.nq : 0, heads = qh + 2 * c.nkv;
+  for (int h0 = lane / TPH; h0 < heads; h0 += RPW * kAppendAhead) {
+    uint4 x0[kAppendAhead], x1[kAppendAhead];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float2 cs = s_cs[tt][c0 * V + e];
-          const float a0 = f0[e], a1 = f1[e];
-          f0[e] = a0 * cs.x - a1 * cs.y;
-          f1[e] = a1 * cs.x + a0 * cs.y;
-        }
-      } else {
+    for (int u = 0; u < kAppendAhead; ++u) {
+      const int hd = h0 + u * RPW;
+      if (hd >= heads) break;
+      const T* src = hd < qh ? static_cast<const T*>(p.q) + (t * c.nq + hd) * D
+                   : hd < qh + c.nkv ? static_cast<const T*>(p.k) + (t * c.nkv + hd - qh) * D
+                                     : static_cast<const T*>(p.v) + (t * c.nkv + hd - qh - c.nkv) * D;
+      x0[u] = *reinterpret_cast<const uint4*>(src + c0 * V);
+      x1[u] = *reinterpret_cast<const uint4*>(src + c1 * V);
+    }
 #pragma unroll
-        for (int e = 0; e < V; e += 2) {
-          const float2 u = s_cs[tt][(c0 * V + e) / 2], w = s_cs[tt][(c1 * V + e) / 2];
-          const float a0 = f0[e], a1 = f0[e + 1], b0 = f1[e], b1 = f1[e + 1];
-          f0[e] = a0 * u.x - a1 * u.y;
-          f0[e + 1] = a1 * u.x + a0 * u.y;
-          f1[e] = b0 * w.x - b1 * w.y;
-          f1[e + 1] = b1 * w.x + b0 * w.y;
-        }
+    for (int u = 0; u < kAppendAhead; ++u) {
+      const int hd = h0 + u * RPW;
+      if (hd >= heads) break;
+      T* dst0 = nullptr;  // token-major output
+      T* dst1 = nullptr;  // page
+      if (hd < qh) {
+        dst0 = static_cast<T*>(p.q_out) + (t * c.nq + hd) * D;
+      } else if (hd < qh + c.nkv) {
+        if (p.k_out) dst0 = static_cast<T*>(p.k_out) + (t * c.nkv + hd - qh) * D;
+        if (pg >= 0) dst1 = static_cast<T*>(c.k_pages) + dst + static_cast<long long>(hd - qh) * c.ps * D;
+      } else if (pg >= 0) {
+        dst1 = static_cast<T*>(c.v_pages) + dst + static_cast<long long>(hd - qh - c.nkv) * c.ps * D;
       }
-      x0 = pack16<T>(f0);
-      x1 = pack16<T>(f1);
-    }
-    if (dst0) {
-      *reinterpret_cast<uint4*>(dst0 + c0 * V) = x0;
-      *reinterpret_cast<uint4*>(dst0 + c1 * V) = x1;
-    }
-    if (dst1) {
-      *reinterpret_cast<uint4*>(dst1 + c0 * V) = x0;
-      *reinterpret_cast<uint4*>(dst1 + c1 * V) = x1;
+      if (hd < qh + c.nkv && turns_here) {
+        float f0[V], f1[V];
+        unpack16<T>(x0[u], f0);
+        unpack16<T>(x1[u], f1);
+        if (p.style == SFA_ROPE_HALF) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float a0 = f0[e], a1 = f1[e];
+            f0[e] = a0 * co[e] - a1 * si[e];
+            f1[e] = a1 * co[e] + a0 * si[e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; e += 2) {
+            const int j = e / 2, k = V / 2 + e / 2;
+            const float a0 = f0[e], a1 = f0[e + 1], b0 = f1[e], b1 = f1[e + 1];
+            f0[e] = a0 * co[j] - a1 * si[j];
+            f0[e + 1] = a1 * co[j] + a0 * si[j];
+            f1[e] = b0 * co[k] - b1 * si[k];
+            f1[e + 1] = b1 * co[k] + b0 * si[k];
+          }
+        }
+        x0[u] = pack16<T>(f0);
+        x1[u] = pack16<T>(f1);
+      }
+      if (dst0) {
+        *reinterpret_cast<uint4*>(dst0 + c0 * V) = x0[u];
+        *reinterpret_cast<uint4*>(dst0 + c1 * V) = x1[u];
+      }
+      if (dst1) {
+        *reinterpret_cast<uint4*>(dst1 + c0 * V) = x0[u];
+        *reinterpret_cast<uint4*>(dst1 + c1 * V) = x1[u];
+      }
     }
   }
 }
@@ -289,13 +284,9 @@ cudaError_t launch_tree_plan(const PlanParams& p, cudaStream_t s) {
   return launch_pdl(tree_plan_kernel, dim3(static_cast<unsigned>(p.B), 1, 1), kPlanThreads, p, s);
 }
 
-cudaError_t launch_kv_append(const AppendParams& in, int in_dtype, int head_dim, int n_sm, cudaStream_t s) {
-  AppendParams p = in;
+cudaError_t launch_kv_append(const AppendParams& p, int in_dtype, int head_dim, cudaStream_t s) {
   const long long total = static_cast<long long>(p.c.Lc) * p.c.B * p.c.n_max;
-  // one token per CTA while the tokens do not fill the card twice, then more
-  p.tokens_per_cta = static_cast<int>(std::min<long long>(kAppendMaxTokens, std::max<long long>(1, total / (8LL * n_sm))));
-  const long long grid = (total + p.tokens_per_cta - 1) / p.tokens_per_cta;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const long long grid = (total + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
   const unsigned g = static_cast<unsigned>(grid);
   if (in_dtype == SFA_F32)
     return head_dim == 64 ? launch_append_t<float, 64>(p, g, s) : launch_append_t<float, 128>(p, g, s);
