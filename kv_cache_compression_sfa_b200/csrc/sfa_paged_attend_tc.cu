@@ -1,9 +1,9 @@
 // sfa_paged_attend_tc.cu — attention of new tokens over the paged cache on the
 // 5th-generation tensor cores (bf16).
 //
-// A CTA walks its run of key tiles (sfa_paged.cuh) with ten working warps:
-//   warp 8     loads: q by one tensor copy per 64 columns, keys and values
-//              page by page into a ring of 128-key buffers;
+// A CTA walks its run of key tiles (sfa_paged.cuh) with eleven working warps:
+//   warps 8, 10  loads: q by one tensor copy per 64 columns, keys (8) and values
+//              (10) page by page into a ring of 128-key buffers;
 //   warp 9     issues the products: S = Q K^T (both operands in shared memory,
 //              K-major), O += P V (P in tensor memory, V MN-major);
 //   warps 0-3  the softmax of stream 0, a thread per row;
@@ -28,14 +28,15 @@
 namespace sfa {
 namespace {
 
-constexpr int kTcThreads = 384;  // ten working warps; registers are dealt out to groups of four
+constexpr int kTcThreads = 384;  // eleven working warps; registers are dealt out to groups of four
 // Registers of a thread after the split: 256 x 208 + 128 x 80 = 63,488, within
 // the 384 x 168 = 64,512 of the launch.  A softmax thread keeps its row's 128
 // scores in registers.
 constexpr int kTcSoftmaxRegs = 208;
 constexpr int kTcOtherRegs = 80;
-constexpr int kTcLoadWarp = 8;
+constexpr int kTcKeyWarp = 8;
 constexpr int kTcMmaWarp = 9;
+constexpr int kTcValueWarp = 10;
 constexpr int kTcKeys = 128;     // keys of a tile
 constexpr int kTcRows = 128;     // rows of a row tile (tensor-memory lanes)
 constexpr uint32_t kTmemCols = 512;
@@ -306,49 +307,53 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
   const int tile_rows = PAIR ? p.rows_step / 2 : p.rows_step;  // rows of one row tile
   bool ok = true;
 
-  if (warp >= kTcLoadWarp) {
+  if (warp >= kTcKeyWarp) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcOtherRegs));
-  if (warp == kTcLoadWarp) {
-    // ---- loads.  Buffer order is the order of use: PAIR K0 V0 K1 V1 ..,
-    // else K0 K1 V0 K2 V1 ..  A lane copies one page's share of one 64-column
-    // block; page ids are read one tile ahead.
+  if (warp == kTcKeyWarp || warp == kTcValueWarp) {
+    // ---- loads: keys and q by one warp, values by another, each into its
+    // buffers of the ring in the order of use: PAIR K0 V0 K1 V1 .., else K0 K1
+    // V0 K2 V1 ..  A lane copies one page's share of one 64-column block; its
+    // page ids are read kIdsAhead tiles ahead and looked at when they are used.
+    constexpr int kIdsAhead = 3;
+    const bool keys = warp == kTcKeyWarp;
+    const CUtensorMap* map = keys ? &maps.k : &maps.v;
     const int prow = min(p.c.ps, kTcKeys);                  // rows of a box
     const int ppt = kTcKeys / prow;                          // pages of a tile
     const int boxes = ppt * (D / 64);
     const int my_page = lane % ppt, my_half = lane / ppt;
     const unsigned box_off = static_cast<unsigned>(my_half * (kTcKeys * 128) + my_page * prow * 128);
     const int z_none = static_cast<int>(static_cast<long long>(p.c.nkv) * p.c.n_pages * (p.c.l0 + p.c.Lc));
-    unsigned n_kv = 0, st = 0, ring_turn = 0;  // buffers filled so far; the next one and its turn
+    unsigned base = 0, last = 0, filled = 0;  // ring position of the piece; of this warp's last buffers
     int n_q = 0;
     for (PieceWalk w(run); w.more() && ok; w.next(p)) {
+      const int n = w.t1 - w.t0;
       const int* table = p.c.table + static_cast<long long>(w.it.b) * p.c.max_pages;
-      const int slot_end = w.it.kv_end;
-      // z coordinate (page and head) of this lane's box in tile t; a box without a key reads as zeros
-      auto coord = [&](int t) -> int {
+      // the slot of this lane's box in tile t, and its page id (raw; -1: no key there, zeros)
+      auto page_id = [&](int t) -> int {
         const int slot = t * kTcKeys + my_page * prow;
-        if (lane >= boxes || t >= w.t1 || slot >= slot_end) return z_none;
-        const int pg = table[slot >> p.c.ps_log2];
-        if (pg < 0 || pg >= p.c.n_pages) {
-          latch_error(p.c.err, SFA_ERR_INVALID_ARG);
-          return z_none;
-        }
-        return static_cast<int>((static_cast<long long>(p.c.l0 + w.it.l) * p.c.n_pages + pg) * p.c.nkv + w.it.kh);
+        return lane < boxes && t < w.t1 && slot < w.it.kv_end ? table[slot >> p.c.ps_log2] : -1;
       };
-      auto fill = [&](const CUtensorMap* map, int t, int z) {
-        if (ring_turn > 0)
-          ok = ok && mbar_wait_bounded(&bars.kv_empty[st], (ring_turn - 1) & 1u, kTcPollLimit, p.c.err);
+      const int z_head = (p.c.l0 + w.it.l) * static_cast<int>(p.c.n_pages);
+      auto fill = [&](int i, int pg) {
+        const unsigned at = base + static_cast<unsigned>(PAIR ? 2 * i + (keys ? 0 : 1) : keys ? (i < 2 ? i : 2 * i - 1)
+                                                                                        : (n == 1 ? 1 : min(2 * i + 2, n + i)));
+        const unsigned st = at % NS, turn = at / NS;
+        if (turn > 0) ok = ok && mbar_wait_bounded(&bars.kv_empty[st], (turn - 1) & 1u, kTcPollLimit, p.c.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
+        const int t = w.t0 + i;
+        int z = z_none;
+        if (pg >= 0 && pg < p.c.n_pages)
+          z = (z_head + pg) * p.c.nkv + w.it.kh;
+        else if (lane < boxes && t * kTcKeys + my_page * prow < w.it.kv_end)
+          latch_error(p.c.err, SFA_ERR_INVALID_ARG);  // a page that is needed: read as zeros
         if (lane == 0) mbar_arrive_expect_tx(&bars.kv_full[st], P::tile);
         __syncwarp();
         if (lane < boxes)
           tma_load_3d(smem + P::ring + st * P::tile + box_off, map, my_half * 64, (t * kTcKeys) & (p.c.ps - 1) & ~(prow - 1), z,
                       &bars.kv_full[st]);
-        ++n_kv;
-        if (++st == NS) {
-          st = 0;
-          ++ring_turn;
-        }
+        last = at;
+        ++filled;
       };
       // q goes behind the item's first keys: its buffer may still be in use
       auto load_q = [&]() {
@@ -369,34 +374,23 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
         __syncwarp();
         ++n_q;
       };
-      const int n = w.t1 - w.t0;
-      if (PAIR) {
-        int z = coord(w.t0);
-        for (int i = 0; i < n && ok; ++i) {
-          const int zn = coord(w.t0 + i + 1);
-          fill(&maps.k, w.t0 + i, z);
-          if (i == 0 && ok) load_q();
-          if (ok) fill(&maps.v, w.t0 + i, z);
-          z = zn;
-        }
-      } else {
-        int z0 = coord(w.t0), z1 = coord(w.t0 + 1), z2 = coord(w.t0 + 2);
-        fill(&maps.k, w.t0, z0);
-        if (n > 1 && ok) fill(&maps.k, w.t0 + 1, z1);
-        if (ok) load_q();
-        for (int i = 0; i < n && ok; ++i) {
-          const int z3 = coord(w.t0 + i + 3);
-          fill(&maps.v, w.t0 + i, z0);
-          if (i + 2 < n && ok) fill(&maps.k, w.t0 + i + 2, z2);
-          z0 = z1;
-          z1 = z2;
-          z2 = z3;
-        }
+      int id[kIdsAhead];
+#pragma unroll
+      for (int j = 0; j < kIdsAhead; ++j) id[j] = page_id(w.t0 + j);
+      const int q_after = PAIR ? 0 : min(n, 2) - 1;  // q follows this tile's keys
+      for (int i = 0; i < n && ok; ++i) {
+        const int next = page_id(w.t0 + i + kIdsAhead);
+        fill(i, id[0]);
+        if (keys && i == q_after && ok) load_q();
+#pragma unroll
+        for (int j = 0; j + 1 < kIdsAhead; ++j) id[j] = id[j + 1];
+        id[kIdsAhead - 1] = next;
       }
+      base += 2u * static_cast<unsigned>(n);
     }
-    if (!ok) {  // no copy may land after the CTA has left
-      for (unsigned i = n_kv > NS ? n_kv - NS : 0u; i < n_kv; ++i)
-        mbar_wait_bounded(&bars.kv_full[i % NS], (i / NS) & 1u, kTcPollLimit, p.c.err);
+    if (!ok) {  // no copy may land after the CTA has left: this warp's fills of the last NS positions
+      for (unsigned at = last < NS ? 0u : last - NS + 1; filled > 0 && at <= last; ++at)
+        mbar_wait_bounded(&bars.kv_full[at % NS], (at / NS) & 1u, kTcPollLimit, p.c.err);
       for (int i = max(0, n_q - q_bufs); i < n_q; ++i)
         mbar_wait_bounded(&bars.q_full[i % q_bufs], static_cast<unsigned>((i / q_bufs) & 1), kTcPollLimit, p.c.err);
     }
