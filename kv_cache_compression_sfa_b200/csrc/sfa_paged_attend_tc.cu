@@ -1,20 +1,27 @@
 // sfa_paged_attend_tc.cu — attention of new tokens over the paged cache on the
 // 5th-generation tensor cores (bf16).
 //
-// A CTA walks its run of key tiles (sfa_paged.cuh) with eleven working warps:
+// A CTA walks its run of key tiles (sfa_paged.cuh) with eleven warps:
 //   warps 8, 10  loads: q by one tensor copy per 64 columns, keys (8) and values
-//              (10) page by page into a ring of 128-key buffers;
-//   warp 9     issues the products: S = Q K^T (both operands in shared memory,
-//              K-major), O += P V (P in tensor memory, V MN-major);
-//   warps 0-3  the softmax of stream 0, a thread per row;
-//   warps 4-7  the softmax of stream 1.
-// The two streams keep the tensor cores busy while one of them computes its
-// softmax.  With more rows than one 128-row tile (PAIR) they are two row tiles
-// that share every key and value tile; with fewer they take the key tiles of
-// one row tile in turn, each with its own maximum, sum and output, which are
-// joined in tensor memory at the end.  P overwrites the scores it came from.
-// Rows are (node, query head of the group), so that one KV head's tile serves
-// all of its query heads.
+//                (10) page by page into a ring of 128-key buffers;
+//   warp 9       issues the products: S = Q K^T (both operands in shared memory,
+//                K-major), O += P V (P in tensor memory, V MN-major);
+//   warps 0-3    the softmax of stream 0, a thread per row;
+//   warps 4-7    the softmax of stream 1.
+// With more rows than one 128-row tile (PAIR) the streams are two row tiles that
+// share every key and value tile; with fewer they take the key tiles of one row
+// tile in turn, each with its own maximum, sum and output, which are joined in
+// tensor memory at the end.  Rows are (node, query head of the group), so that
+// one KV head's tile serves all of its query heads.
+//
+// Scores, P and their products go by steps: a whole tile with PAIR, where the
+// other stream's products fill the time of a softmax, and half a tile without,
+// so that a stream's products of one half run under the softmax of its other.
+// P overwrites the scores that it came from.  A product with q in shared memory
+// costs about as much for 64 keys as for 128 (it reads all of q), so PAIR, bound
+// by the tensor cores and the softmax together, loses by half steps what it gains
+// in overlap: 172 against 160 us (37 sequences of 8,192 tokens, 36 new ones
+// each); 64 keys of a row per thread with two threads a row took 260 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -28,19 +35,19 @@
 namespace sfa {
 namespace {
 
-constexpr int kTcThreads = 384;  // eleven working warps; registers are dealt out to groups of four
+constexpr int kTcThreads = 384;  // warp 11 only fills the last group of four
 // Registers of a thread after the split: 256 x 208 + 128 x 80 = 63,488, within
-// the 384 x 168 = 64,512 of the launch.  A softmax thread keeps its row's 128
-// scores in registers.
+// the 384 x 168 = 64,512 of the launch.
 constexpr int kTcSoftmaxRegs = 208;
 constexpr int kTcOtherRegs = 80;
+constexpr int kTcSoftmaxThreads = 256;
 constexpr int kTcKeyWarp = 8;
 constexpr int kTcMmaWarp = 9;
 constexpr int kTcValueWarp = 10;
 constexpr int kTcKeys = 128;     // keys of a tile
 constexpr int kTcRows = 128;     // rows of a row tile (tensor-memory lanes)
 constexpr uint32_t kTmemCols = 512;
-constexpr unsigned kTcPollLimit = 1u << 22;  // polls of a bounded wait
+constexpr unsigned kTcPollLimit = 1u << 20;  // polls of a bounded wait
 constexpr float kRescaleLog2 = 8.0f;  // the maximum moves only when it grows by more than this (log2)
 
 // Shared memory: q (one row tile, or two), then the ring; all blocks
@@ -52,6 +59,10 @@ struct TcPlan {
   static constexpr int ring = (PAIR ? 2 : 1) * tile;
   static constexpr int stages = D == 128 ? (PAIR ? 5 : 6) : (PAIR ? 11 : 12);
   static constexpr int shared = ring + stages * tile;   // TcShared
+  // Keys of a step: scores, P and their products go by steps, each with its
+  // own columns of tensor memory.
+  static constexpr int step = PAIR ? 128 : 64;
+  static constexpr int steps = kTcKeys / step;
 };
 
 struct TcMaps {
@@ -61,7 +72,9 @@ struct TcMaps {
 struct TcBars {
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[12], kv_empty[12];
-  uint64_t s_full[2], p_full[2], o_done[2], drain;
+  uint64_t s_full[2][2], p_full[2][2];  // [stream][half]
+  uint64_t o_step[2];                   // a step is added to the stream's output
+  uint64_t o_done[2], drain;            // the piece's last one (PAIR: of each stream, else of both)
 };
 
 struct TcShared {
@@ -160,14 +173,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// P of a row's 128 scores into 64 columns of tensor memory; returns its sum.  P
-// is rounded to bf16 for the tensor cores (off by 2^-9 at most, half a step,
-// as much as the result's own rounding); the sum keeps 32 bits.
+// P of N scores into N / 2 columns of tensor memory; returns its sum.  P is rounded
+// to bf16 for the tensor cores (off by 2^-9 of its size on average, as much as
+// the result's own rounding); the sum keeps 32 bits.
+template <int N>
 __device__ __forceinline__ float store_probs(float* x, float scale, float base, uint32_t taddr) {
   const float2 sc = make_float2(scale, scale), nb = make_float2(-base, -base);
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-  for (int c = 0; c < kTcKeys; c += 64) {
+  for (int c = 0; c < N; c += 64) {
     uint32_t w[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
@@ -182,32 +196,35 @@ __device__ __forceinline__ float store_probs(float* x, float scale, float base, 
   return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
-// Visibility of tile t's keys to one row: keys below `end`, and of the new
-// tokens those of the row's mask words (tree).  The words are loaded before
-// the scores are waited for.
+// Visibility of N keys from slot `slot` on to one row: those below `end`, and
+// of the new tokens those of the row's mask words (tree).  The words are loaded
+// before the scores are waited for.
+template <int N>
 struct RowMask {
-  uint32_t w[kTcKeys / 32 + 1];
+  uint32_t w[N / 32 + 1];
   int end, shift;
 };
 
-__device__ __forceinline__ RowMask row_mask(const AttendParams& p, const AttendItem& it, int node, int t) {
-  RowMask r;
-  r.end = p.mask ? it.ctx + it.len : it.ctx + min(node + 1, it.len);
-  const int rel = t * kTcKeys - it.ctx;
+template <int N>
+__device__ __forceinline__ RowMask<N> row_mask(const AttendParams& p, const AttendItem& it, int node, int slot) {
+  RowMask<N> r;
+  r.end = (p.mask ? it.ctx + it.len : it.ctx + min(node + 1, it.len)) - slot;
+  const int rel = slot - it.ctx;
   const int w0 = rel >> 5;
   r.shift = rel & 31;
   const uint32_t* m = p.mask + (static_cast<long long>(it.b) * p.c.n_max + node) * p.words;
 #pragma unroll
-  for (int i = 0; i < kTcKeys / 32 + 1; ++i) {
+  for (int i = 0; i < N / 32 + 1; ++i) {
     r.w[i] = 0xffffffffu;  // the context
     if (p.mask && w0 + i >= 0) r.w[i] = w0 + i < p.words ? m[w0 + i] : 0u;
   }
   return r;
 }
 
-// Bit i: key t * 128 + 32 * c + i is visible.
-__device__ __forceinline__ uint32_t visible_bits(const RowMask& r, int t, int c) {
-  const int n = r.end - (t * kTcKeys + 32 * c);
+// Bit i: key 32 * c + i of them is visible.
+template <int N>
+__device__ __forceinline__ uint32_t visible_bits(const RowMask<N>& r, int c) {
+  const int n = r.end - 32 * c;
   const uint32_t below = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
   return below & __funnelshift_r(r.w[c], r.w[c + 1], r.shift);
 }
@@ -269,7 +286,7 @@ template <int D, bool PAIR>
 __global__ void __launch_bounds__(kTcThreads, 1)
 attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ TcMaps maps) {
   using P = TcPlan<D, PAIR>;
-  constexpr int NS = P::stages;
+  constexpr int NS = P::stages, HK = P::step, NH = P::steps;
   // the kernel has no other shared memory: the dynamic block starts on the 1024
   // bytes that the swizzled tiles need
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -286,8 +303,11 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       mbar_init(&bars.kv_empty[i], 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars.s_full[s], 1);
-      mbar_init(&bars.p_full[s], 4);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&bars.s_full[s][h], 1);
+        mbar_init(&bars.p_full[s][h], 4);
+      }
+      mbar_init(&bars.o_step[s], 1);
       mbar_init(&bars.o_done[s], 1);
       sh.bad[s] = 0;
     }
@@ -308,7 +328,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
   bool ok = true;
 
   if (warp >= kTcKeyWarp) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcOtherRegs));
+  if constexpr (PAIR) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcOtherRegs));
   if (warp == kTcKeyWarp || warp == kTcValueWarp) {
     // ---- loads: keys and q by one warp, values by another, each into its
     // buffers of the ring in the order of use: PAIR K0 V0 K1 V1 .., else K0 K1
@@ -399,7 +419,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
     // uniform; one elected lane issues.
     {
       const bool leader = elect_one();
-      const uint32_t idesc_qk = umma_idesc_bf16(kTcRows, kTcKeys, false);
+      const uint32_t idesc_qk = umma_idesc_bf16(kTcRows, HK, false);
       const uint32_t idesc_pv = umma_idesc_bf16(kTcRows, D, true);
       const uint64_t d_q = desc_sw128(smem_u32(smem + P::q), 16, 1024);
       const uint64_t d_k = desc_sw128(smem_u32(smem + P::ring), 16, 1024);
@@ -410,7 +430,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       unsigned n_p[2] = {0u, 0u};
       auto wait = [&](uint64_t* bar, unsigned parity) {
         ok = ok && mbar_wait_bounded(bar, parity & 1u, kTcPollLimit, p.c.err);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = __all_sync(0xffffffffu, ok);  // no lane may fall two phases behind
         tc_fence_after();
         return ok;
       };
@@ -427,25 +447,30 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       auto commit = [&](uint64_t* bar) {
         if (leader) umma_commit(bar);
       };
-      auto qk = [&](int s, int st, uint64_t q_desc) {
-        const uint64_t a = q_desc + (PAIR ? s * (P::tile >> 4) : 0), b = d_k + st * (P::tile >> 4);
-        const uint32_t d = tmem + static_cast<uint32_t>(s) * kTcKeys;
+      // scores of half h of the keys in buffer st
+      auto qk = [&](int s, int h, int st, uint64_t q_desc) {
+        const uint64_t a = q_desc + (PAIR ? s * (P::tile >> 4) : 0);
+        const uint64_t b = d_k + ((st * P::tile + h * (HK * 128)) >> 4);
+        const uint32_t d = tmem + static_cast<uint32_t>(s * kTcKeys + h * HK);
         if (leader) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t off = ((k >> 2) * (kTcKeys * 128) + (k & 3) * 32) >> 4;
             umma_bf16(d, a + off, b + off, idesc_qk, k > 0);
           }
-          umma_commit(&bars.s_full[s]);
+          umma_commit(&bars.s_full[s][h]);
         }
       };
-      auto pv = [&](int s, int st, bool first) {
-        const uint64_t b = d_v + st * (P::tile >> 4);
-        const uint32_t d = tmem + 256u + static_cast<uint32_t>(s) * D, a = tmem + static_cast<uint32_t>(s) * kTcKeys;
+      // their P times the values in buffer st
+      auto pv = [&](int s, int h, int st, bool first) {
+        const uint64_t b = d_v + ((st * P::tile + h * (HK * 128)) >> 4);
+        const uint32_t d = tmem + 256u + static_cast<uint32_t>(s) * D;
+        const uint32_t a = tmem + static_cast<uint32_t>(s * kTcKeys + h * HK);
         if (leader) {
 #pragma unroll
-          for (int k = 0; k < kTcKeys / 16; ++k)
+          for (int k = 0; k < HK / 16; ++k)
             umma_bf16_ts(d, a + k * 8, b + ((k * 2048) >> 4), idesc_pv, k > 0 || !first);
+          if (NH > 1) umma_commit(&bars.o_step[s]);
         }
       };
       for (PieceWalk w(run); w.more() && ok; w.next(p)) {
@@ -454,55 +479,58 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
         if (!wait(&bars.q_full[qb], static_cast<unsigned>(n_q / q_bufs))) break;
         ++n_q;
         const uint64_t d_qb = d_q + (qb * (kTcRows / 2 * 128) >> 4);
-        int st_k, st_v;
+        int st_k = 0, st_v = 0;
         if (PAIR) {
           if (!next_kv(&st_k)) break;
-          qk(0, st_k, d_qb);
-          qk(1, st_k, d_qb);
+#pragma unroll
+          for (int hs = 0; hs < 2 * NH; ++hs) qk(hs & 1, hs >> 1, st_k, d_qb);
           commit(&bars.kv_empty[st_k]);
           if (n == 1) commit(&bars.q_empty[qb]);
-          for (int i = 0; i < n; ++i) {
+          for (int i = 0; i < n && ok; ++i) {
+            const bool more = i + 1 < n;
             if (!next_kv(&st_v)) break;
-            if (!wait(&bars.p_full[0], n_p[0]++)) break;
-            pv(0, st_v, i == 0);
-            if (i + 1 < n) {
-              if (!next_kv(&st_k)) break;
-              qk(0, st_k, d_qb);
-            } else {
-              commit(&bars.o_done[0]);
+#pragma unroll
+            for (int hs = 0; hs < 2 * NH; ++hs) {  // a step of both streams, then the next
+              const int h = hs >> 1, s = hs & 1;
+              if (!wait(&bars.p_full[s][h], n_p[s])) continue;
+              pv(s, h, st_v, i == 0 && h == 0);
+              if (more && hs == 0 && !next_kv(&st_k)) continue;
+              if (more) qk(s, h, st_k, d_qb);
             }
-            if (!wait(&bars.p_full[1], n_p[1]++)) break;
-            pv(1, st_v, i == 0);
+            if (!ok) break;
+            ++n_p[0];
+            ++n_p[1];
             commit(&bars.kv_empty[st_v]);
-            if (i + 1 < n) {
-              qk(1, st_k, d_qb);
-              commit(&bars.kv_empty[st_k]);
-              if (i + 2 == n) commit(&bars.q_empty[qb]);
-            } else {
-              commit(&bars.o_done[1]);
-            }
+            if (more) commit(&bars.kv_empty[st_k]);
+            if (i + 2 == n) commit(&bars.q_empty[qb]);
+            if (!more)
+              for (int s = 0; s < 2; ++s) commit(&bars.o_done[s]);
           }
         } else {
           for (int i = 0; i < min(n, 2) && ok; ++i) {
             if (!next_kv(&st_k)) break;
-            qk(i, st_k, d_qb);
+            for (int h = 0; h < NH; ++h) qk(i, h, st_k, d_qb);
             commit(&bars.kv_empty[st_k]);
           }
           if (!ok) break;
           if (n <= 2) commit(&bars.q_empty[qb]);
-          for (int i = 0; i < n; ++i) {
+          for (int i = 0; i < n && ok; ++i) {
             const int s = i & 1;
+            const bool more = i + 2 < n;
             if (!next_kv(&st_v)) break;
-            if (!wait(&bars.p_full[s], n_p[s]++)) break;
-            pv(s, st_v, i < 2);
-            commit(&bars.kv_empty[st_v]);
-            if (i + 2 < n) {
-              if (!next_kv(&st_k)) break;
-              qk(s, st_k, d_qb);
-              commit(&bars.kv_empty[st_k]);
-              if (i + 3 == n) commit(&bars.q_empty[qb]);
+            for (int h = 0; h < NH && ok; ++h) {
+              if (!wait(&bars.p_full[s][h], n_p[s])) break;
+              pv(s, h, st_v, i < 2 && h == 0);
+              if (more && h == 0 && !next_kv(&st_k)) break;
+              if (more) qk(s, h, st_k, d_qb);
             }
+            if (!ok) break;
+            ++n_p[s];
+            commit(&bars.kv_empty[st_v]);
+            if (more) commit(&bars.kv_empty[st_k]);
+            if (i + 3 == n) commit(&bars.q_empty[qb]);
           }
+          if (!ok) break;
           commit(&bars.o_done[0]);
         }
         if (!ok) break;
@@ -515,14 +543,13 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
     __syncwarp();
   }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcSoftmaxRegs));
+    if constexpr (PAIR) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcSoftmaxRegs));
     // ---- softmax of stream s, a thread per row
     const int s = warp >> 2, sub = warp & 3;
     const int r = sub * 32 + lane;  // row of the tile, tensor-memory lane
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(sub * 32) << 16);
-    const uint32_t t_s = lane_base + static_cast<uint32_t>(s) * kTcKeys;
     const uint32_t t_o = lane_base + 256u + static_cast<uint32_t>(s) * D;
-    unsigned n_s = 0, n_piece = 0;
+    unsigned n_t = 0, n_o = 0, n_piece = 0;  // tiles and steps of this stream, and pieces, so far
     unsigned n_kv = 0;  // ring position of the piece's first buffer
     bool wrote = false;
     // after a wait that ran out a warp only keeps the CTA's barriers company
@@ -532,91 +559,98 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       const int row0 = it.row0 + (PAIR ? s * tile_rows : 0);
       const int rows = min(tile_rows, it.rows - (PAIR ? s * tile_rows : 0));  // <= 0: an empty second tile
       const bool warp_live = sub * 32 < rows;
-      const int node = min((row0 + r) / p.c.G, max(it.len - 1, 0));
+      const int nd = (row0 + r) / p.c.G, node = min(nd, max(it.len - 1, 0));
       // keys below this are visible to every row of the piece
       const int full_end = p.mask ? it.ctx : it.ctx + it.row0 / p.c.G + 1;
       float m = -INFINITY, l = 0.f;
       for (int i = PAIR ? 0 : s; i < n && ok; i += PAIR ? 1 : 2) {
         const int t = w.t0 + i;
-        const bool first = i < 2 && (PAIR ? i == 0 : true);
         const bool masked = (t + 1) * kTcKeys > full_end;
-        RowMask vis;
-        if (masked) {
-          vis = row_mask(p, it, node, t);
-          if (!PAIR || s == 0) {
-            // this tile's values: their buffer's place in the loader's order
-            const unsigned at = n_kv + static_cast<unsigned>(PAIR ? 2 * i + 1 : (n == 1 ? 1 : min(2 * i + 2, n + i)));
-            const unsigned st = at % NS;
-            ok = mbar_wait_bounded(&bars.kv_full[st], (at / NS) & 1u, kTcPollLimit, p.c.err);
-            if (!__all_sync(0xffffffffu, ok)) {
-              ok = false;
-              break;
-            }
-            clean_values<D>(smem + P::ring + st * P::tile, full_end - t * kTcKeys, it.kv_end - t * kTcKeys, r, &sh.bad[s]);
-          }
+        if (masked && (!PAIR || s == 0)) {
+          // this tile's values: their buffer's place in the loader's order
+          const unsigned at = n_kv + static_cast<unsigned>(PAIR ? 2 * i + 1 : (n == 1 ? 1 : min(2 * i + 2, n + i)));
+          const unsigned st = at % NS;
+          ok = mbar_wait_bounded(&bars.kv_full[st], (at / NS) & 1u, kTcPollLimit, p.c.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          clean_values<D>(smem + P::ring + st * P::tile, full_end - t * kTcKeys, it.kv_end - t * kTcKeys, r, &sh.bad[s]);
         }
-        ok = mbar_wait_bounded(&bars.s_full[s], n_s & 1u, kTcPollLimit, p.c.err);
-        ++n_s;
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (warp_live) {
-          float x[kTcKeys];
-#pragma unroll
-          for (int c = 0; c < kTcKeys; c += 32) tmem_ld32_async(t_s + c, x + c);
-          tmem_ld_wait<kTcKeys>(x);
-          if (masked) {
-#pragma unroll
-            for (int c = 0; c < kTcKeys; c += 32) {
-              const uint32_t bits = visible_bits(vis, t, c / 32);
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!((bits >> j) & 1u)) x[c + j] = -INFINITY;
-            }
-          }
-          float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-          for (int j = 4; j + 1 < kTcKeys; j += 2) mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], x[j], x[j + 1]);
-          const float top = max3(mx[0], mx[1], max3(mx[2], mx[3], mx[3])) * p.scale_log2;
-          // the maximum in use may lag behind by 2^8, which fp32 sums and outputs hold easily
-          const bool move = !(top <= m + kRescaleLog2);  // a NaN score moves it to NaN, and the row with it
-          float fix = 1.f;
-          if (move) {
-            fix = exp2_approx(m - top);
-            m = top;
-            l *= fix;
-          }
-          if (!first && __any_sync(0xffffffffu, move && r < rows)) {
-            float o[32];
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              tmem_ld32_async(t_o + c, o);
-              tmem_ld_wait<32>(o);
+        for (int h = 0; h < NH; ++h) {
+          const bool first = h == 0 && (PAIR ? i == 0 : i < 2);
+          RowMask<HK> vis;
+          if (masked) vis = row_mask<HK>(p, it, node, t * kTcKeys + h * HK);
+          ok = mbar_wait_bounded(&bars.s_full[s][h], n_t & 1u, kTcPollLimit, p.c.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          if (warp_live) {
+            const uint32_t t_s = lane_base + static_cast<uint32_t>(s * kTcKeys + h * HK);
+            float x[HK];
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] *= fix;
-              tmem_st32(t_o + c, reinterpret_cast<const uint32_t*>(o));
+            for (int c = 0; c < HK; c += 32) tmem_ld32_async(t_s + c, x + c);
+            tmem_ld_wait<HK>(x);
+            if (masked) {
+#pragma unroll
+              for (int c = 0; c < HK / 32; ++c) {
+                const uint32_t bits = visible_bits(vis, c);
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (!((bits >> j) & 1u)) x[c * 32 + j] = -INFINITY;
+              }
             }
+            float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+            for (int j = 4; j + 1 < HK; j += 2) mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], x[j], x[j + 1]);
+            const float top = max3(mx[0], mx[1], max3(mx[2], mx[3], mx[3])) * p.scale_log2;
+            // the maximum in use may lag behind by 2^8, which fp32 sums and outputs hold easily
+            const bool move = !(top <= m + kRescaleLog2);  // a NaN score moves it to NaN, and the row with it
+            float fix = 1.f;
+            if (move) {
+              fix = exp2_approx(m - top);
+              m = top;
+              l *= fix;
+            }
+            if (!first && __any_sync(0xffffffffu, move && r < rows)) {
+              // O holds the step before the last of this stream (these scores came
+              // after it); with two steps a tile the last one is waited for
+              if (NH > 1) {
+                ok = mbar_wait_bounded(&bars.o_step[s], (n_o - 1u) & 1u, kTcPollLimit, p.c.err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+              }
+              tc_fence_after();
+              float o[32];
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                tmem_ld32_async(t_o + c, o);
+                tmem_ld_wait<32>(o);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] *= fix;
+                tmem_st32(t_o + c, reinterpret_cast<const uint32_t*>(o));
+              }
+            }
+            l += store_probs<HK>(x, p.scale_log2, m == -INFINITY ? 0.f : m, t_s);
+            tmem_st_wait();
           }
-          const float base = m == -INFINITY ? 0.f : m;
-          l += store_probs(x, p.scale_log2, base, t_s);
-          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.p_full[s][h]);
+          ++n_o;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p_full[s]);
+        if (!ok) break;
+        ++n_t;
       }
       n_kv += 2u * static_cast<unsigned>(n);
       // ---- result of the piece
       const bool starts = w.t0 == 0, whole = starts && w.t1 == it.nt;
-      if (!PAIR) {
-        sh.ml[s][r] = make_float2(m, l);
-        named_bar_sync(1, 256);
-      }
       ok = ok && mbar_wait_bounded(&bars.o_done[PAIR ? s : 0], n_piece & 1u, kTcPollLimit, p.c.err);
       ++n_piece;
       ok = __all_sync(0xffffffffu, ok);
+      if (!PAIR) {
+        sh.ml[s][r] = make_float2(m, l);
+        named_bar_sync(1, kTcSoftmaxThreads);
+      }
       if (ok) {
         tc_fence_after();
         float w0 = 1.f, w1 = 0.f;
@@ -632,7 +666,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
         const int slot0 = max(w.t0 * kTcKeys, full_end);
         const int slot1 = min(w.t1 * kTcKeys, it.kv_end);
         const float inv = l == 0.f ? 0.f : 1.0f / l;
-        const int g_row = row0 + r, nd = g_row / p.c.G, g = g_row - nd * p.c.G;
+        const int g = row0 + r - nd * p.c.G;
         constexpr int NC = PAIR ? D : D / 2;  // columns of this warp group
         constexpr int W = NC < 64 ? NC : 64;  // columns at a time
         const int c0 = PAIR ? 0 : s * NC;
@@ -697,9 +731,9 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
         tc_fence_before();
       }
       // outputs and flags are read: the next piece may overwrite them
-      named_bar_sync(1, 256);
+      named_bar_sync(1, kTcSoftmaxThreads);
       if (tid == 0) sh.bad[0] = sh.bad[1] = 0;
-      named_bar_sync(1, 256);
+      named_bar_sync(1, kTcSoftmaxThreads);
     }
     if (!wrote && tid == 0) write_meta(p, run, false, run.it, 0);
   }
