@@ -800,8 +800,7 @@ int sfa_kv_attend(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begi
                   void* workspace, size_t workspace_bytes, void* stream) {
   int st = paged_status(h, n_max, ctx_lens, batch);
   if (st != SFA_OK) return st;
-  AttendParams p;
-  std::memset(&p, 0, sizeof(p));
+  AttendParams p = {};
   st = fill_paged(p.c, h, cache, layer_begin, layer_count, n_max, lens, ctx_lens, batch);
   if (st != SFA_OK) return st;
   if (n_max == 0) return SFA_OK;
@@ -826,6 +825,10 @@ int sfa_kv_attend(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begi
   p.words = (n_max + 31) / 32;
   p.rows_step = a.rows_step;
   p.kt = a.kt;
+  while ((1 << p.kt_log2) < a.kt) ++p.kt_log2;
+  p.by_group = FastDiv(static_cast<unsigned>(p.c.G));
+  p.by_rows = FastDiv(static_cast<unsigned>(a.rows_step));
+  p.by_ctas = FastDiv(static_cast<unsigned>(a.n_cta));
   p.n_cta = a.n_cta;
   p.item_cost = a.item_cost;
   p.spread = kAttendSpread;

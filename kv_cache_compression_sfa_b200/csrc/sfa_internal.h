@@ -247,6 +247,24 @@ struct SplitMeta {
   int pad[2];
 };
 
+// Division of 0 <= n < 2^31 by a constant of the call: (n * mul) >> (32 + shift).
+struct FastDiv {
+  unsigned d, mul, shift;
+  FastDiv(unsigned divisor = 1) : d(divisor), mul(0), shift(0) {
+    unsigned l = 0;
+    while ((1ull << l) < divisor) ++l;  // 2^l >= divisor
+    if (divisor > 1) {
+      mul = static_cast<unsigned>(((1ull << (31 + l)) + divisor - 1) / divisor);
+      shift = l - 1;
+    }
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int operator()(int n) const {
+    return d == 1 ? n : static_cast<int>(__umulhi(static_cast<unsigned>(n), mul) >> shift);
+  }
+#endif
+};
+
 struct AttendParams {
   PagedParams c;
   const void* q;
@@ -254,7 +272,8 @@ struct AttendParams {
   const uint32_t* mask;     // [B][n_max][words], or null: causal
   int words;
   int rows_step;            // rows (node * G + head) of a work item
-  int kt;                   // keys of a tile
+  int kt, kt_log2;          // keys of a tile
+  FastDiv by_group, by_rows, by_ctas;  // by c.G, rows_step and n_cta
   int n_cta;                // CTAs that share the tiles
   int item_cost, spread;    // tiles that an item's start and result weigh, from `spread` tiles a CTA on
   float scale_log2;         // log2(e) / sqrt(d)

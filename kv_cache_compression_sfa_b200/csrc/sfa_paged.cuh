@@ -68,21 +68,26 @@ struct AttendRun {
 };
 
 __device__ __forceinline__ int row_tiles(const AttendParams& p, int len) {
-  return (len * p.c.G + p.rows_step - 1) / p.rows_step;
+  return p.by_rows(len * p.c.G + p.rows_step - 1);
+}
+
+// Key tiles that cover keys 0 .. n - 1.
+__device__ __forceinline__ int tiles_up_to(const AttendParams& p, int n) {
+  return static_cast<int>((static_cast<unsigned>(n) + static_cast<unsigned>(p.kt) - 1u) >> p.kt_log2);
 }
 
 // Keys that any row of row tile rt sees.
 __device__ __forceinline__ int kv_end_of(const AttendParams& p, int ctx, int len, int rt) {
   if (p.mask) return ctx + len;
   const int row_end = min((rt + 1) * p.rows_step, len * p.c.G);
-  return ctx + (row_end - 1) / p.c.G + 1;
+  return ctx + p.by_group(row_end - 1) + 1;
 }
 
 __device__ __forceinline__ void set_item(const AttendParams& p, AttendItem& it) {
   it.row0 = it.rt * p.rows_step;
   it.rows = min(p.rows_step, it.len * p.c.G - it.row0);
   it.kv_end = kv_end_of(p, it.ctx, it.len, it.rt);
-  it.nt = (it.kv_end + p.kt - 1) / p.kt;
+  it.nt = tiles_up_to(p, it.kv_end);
 }
 
 // The item after `it`; only called where one follows.
@@ -105,7 +110,7 @@ __device__ __forceinline__ void next_item(const AttendParams& p, AttendItem& it)
 }
 
 __device__ __forceinline__ int tiles_of(const AttendParams& p, int ctx, int len, int rt) {
-  return (kv_end_of(p, ctx, len, rt) + p.kt - 1) / p.kt;
+  return tiles_up_to(p, kv_end_of(p, ctx, len, rt));
 }
 
 __device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive
@@ -120,7 +125,7 @@ __device__ __forceinline__ int warp_scan(int v, int lane) {  // inclusive
 // Tiles of one KV head of sequence s, by one thread (few row tiles).
 __device__ __forceinline__ int seq_tiles(const AttendParams& p, const SeqLens& s) {
   const int nrt = row_tiles(p, s.len);
-  if (p.mask) return nrt * ((s.ctx + s.len + p.kt - 1) / p.kt);
+  if (p.mask || nrt <= 1) return nrt * tiles_up_to(p, s.ctx + s.len);
   int n = 0;
   for (int rt = 0; rt < nrt; ++rt) n += tiles_of(p, s.ctx, s.len, rt);
   return n;
@@ -142,17 +147,18 @@ __device__ __forceinline__ AttendRun find_run(const AttendParams& p, bool latch)
   const int B = p.c.B, nkv = p.c.nkv;
   const bool wide = !p.mask && row_tiles(p, p.c.n_max) > 8;
   const int per = (B + 31) >> 5, b0 = min(B, lane * per), b1 = min(B, b0 + per);
+  SeqLens s = {0, 0};  // of this lane's last sequence
   int mine = 0, rows = 0, layer, items;  // tiles and row tiles of one KV head: of this lane's sequences, of all
   if (wide) {
     layer = items = 0;
     for (int b = 0; b < B; ++b) {
-      const SeqLens s = seq_lens(p.c, b, latch && lane == 0);
+      s = seq_lens(p.c, b, latch && lane == 0);
       layer += seq_tiles_warp(p, s, lane);
       items += row_tiles(p, s.len);
     }
   } else {
     for (int b = b0; b < b1; ++b) {
-      const SeqLens s = seq_lens(p.c, b, latch);
+      s = seq_lens(p.c, b, latch);
       mine += seq_tiles(p, s);
       rows += row_tiles(p, s.len);
     }
@@ -167,16 +173,15 @@ __device__ __forceinline__ AttendRun find_run(const AttendParams& p, bool latch)
   layer += c * items;
   mine += c * rows;
   const int total = layer * nkv * p.c.Lc;
-  r.chunk = max(1, (total + p.n_cta - 1) / p.n_cta);
+  r.chunk = max(1, p.by_ctas(total + p.n_cta - 1));
   const long long first = static_cast<long long>(blockIdx.x) * r.chunk;
   r.first = static_cast<int>(min(first, static_cast<long long>(total)));
   r.units = min(r.chunk, total - r.first);
   r.unit = 0;
   if (r.units <= 0) return r;
-  const int l = r.first / (layer * nkv);
+  const int l = p.c.Lc > 1 ? r.first / (layer * nkv) : 0;
   int rem = r.first - l * layer * nkv;  // unit within the layer
   // the sequence: prefix sums count one KV head, the order within a sequence is row tile, KV head
-  SeqLens s;
   int b = 0;
   if (wide) {
     for (;; ++b) {
@@ -197,8 +202,9 @@ __device__ __forceinline__ AttendRun find_run(const AttendParams& p, bool latch)
         if (rem < n) break;
         rem -= n;
       }
-    } else {
-      s = seq_lens(p.c, b, false);
+    } else {  // a sequence per lane: the lane has its lengths
+      s.ctx = __shfl_sync(0xffffffffu, s.ctx, src);
+      s.len = __shfl_sync(0xffffffffu, s.len, src);
     }
   }
   r.it.l = l;
@@ -207,10 +213,12 @@ __device__ __forceinline__ AttendRun find_run(const AttendParams& p, bool latch)
   r.it.len = s.len;
   const int nrt = row_tiles(p, s.len);
   int rt = 0, nt = 0;  // nt: units of the row tile
-  if (p.mask) {
-    nt = (s.ctx + s.len + p.kt - 1) / p.kt + c;
-    rt = rem / (nt * nkv);
-    rem -= rt * nt * nkv;
+  if (p.mask || nrt == 1) {
+    nt = tiles_up_to(p, s.ctx + s.len) + c;
+    if (nrt > 1) {
+      rt = rem / (nt * nkv);
+      rem -= rt * nt * nkv;
+    }
   } else {
     for (int base = 0; base < nrt; base += 32) {  // the row tile that holds the remainder, 32 at a time
       const int t = base + lane < nrt ? tiles_of(p, s.ctx, s.len, base + lane) + c : 0;
@@ -227,7 +235,7 @@ __device__ __forceinline__ AttendRun find_run(const AttendParams& p, bool latch)
     }
   }
   r.it.rt = rt;
-  r.it.kh = rem / nt;
+  r.it.kh = nkv > 1 ? rem / nt : 0;
   r.unit = rem - r.it.kh * nt;
   set_item(p, r.it);
   return r;

@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attend_simt_kernel(const __gr
       const int r = a / (D / 4), d4 = (a - r * (D / 4)) * 4;
       float f[4] = {0.f, 0.f, 0.f, 0.f};
       if (r < it.rows) {
-        const int row = it.row0 + r, node = row / p.c.G, g = row - node * p.c.G;
+        const int row = it.row0 + r, node = p.by_group(row), g = row - node * p.c.G;
         const long long off = (((static_cast<long long>(it.l) * p.c.B + it.b) * p.c.n_max + node) * p.c.nq +
                                it.kh * p.c.G + g) * D + d4;
         VecLoad<T, 4>::run(static_cast<const T*>(p.q) + off, f);
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attend_simt_kernel(const __gr
       for (int r = 0; r < RPW; ++r) {
         if (edge) {
           const int row = it.row0 + warp * RPW + r;
-          const int node = min(row / p.c.G, max(it.len - 1, 0));
+          const int node = min(p.by_group(row), max(it.len - 1, 0));
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int rel = t * kSimtKeys + lane + 32 * u - it.ctx;
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attend_simt_kernel(const __gr
       const int rr = warp * RPW + r;
       if (rr >= it.rows) continue;
       if (whole) {
-        const int row = it.row0 + rr, node = row / p.c.G, g = row - node * p.c.G;
+        const int row = it.row0 + rr, node = p.by_group(row), g = row - node * p.c.G;
         T* dst = static_cast<T*>(p.out) + (((static_cast<long long>(it.l) * p.c.B + it.b) * p.c.n_max + node) * p.c.nq +
                                            it.kh * p.c.G + g) * D + lane * DPL;
         const float inv = sum == 0.f ? 0.f : 1.0f / sum;  // a row that sees nothing is zero
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(256) attend_combine_kernel(const __grid_consta
     for (int e = 0; e < DPL; ++e) o[e] = some ? fmaf(v[e], w, o[e]) : o[e];
   }
   const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-  const int row = m.row0 + r, node = row / p.c.G, g = row - node * p.c.G;
+  const int row = m.row0 + r, node = p.by_group(row), g = row - node * p.c.G;
   T* dst = static_cast<T*>(p.out) + (((static_cast<long long>(m.l) * p.c.B + m.b) * p.c.n_max + node) * p.c.nq +
                                      m.kh * p.c.G + g) * D + lane * DPL;
 #pragma unroll

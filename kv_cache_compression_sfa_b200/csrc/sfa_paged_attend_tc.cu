@@ -382,8 +382,8 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
           ok = ok && mbar_wait_bounded(&bars.q_empty[qb], static_cast<unsigned>((turn - 1) & 1), kTcPollLimit, p.c.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
-        const int node0 = w.it.row0 / p.c.G;
-        const int nb = tile_rows / p.c.G;
+        const int node0 = p.by_group(w.it.row0);
+        const int nb = p.by_group(tile_rows);
         if (lane == 0) {
           mbar_arrive_expect_tx(&bars.q_full[qb], static_cast<unsigned>(tile_rows * 128 * (D / 64) * (PAIR ? 2 : 1)));
           for (int s = 0; s < (PAIR ? 2 : 1); ++s)
@@ -559,9 +559,9 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       const int row0 = it.row0 + (PAIR ? s * tile_rows : 0);
       const int rows = min(tile_rows, it.rows - (PAIR ? s * tile_rows : 0));  // <= 0: an empty second tile
       const bool warp_live = sub * 32 < rows;
-      const int nd = (row0 + r) / p.c.G, node = min(nd, max(it.len - 1, 0));
+      const int nd = p.by_group(row0 + r), node = min(nd, max(it.len - 1, 0));
       // keys below this are visible to every row of the piece
-      const int full_end = p.mask ? it.ctx : it.ctx + it.row0 / p.c.G + 1;
+      const int full_end = p.mask ? it.ctx : it.ctx + p.by_group(it.row0) + 1;
       float m = -INFINITY, l = 0.f;
       for (int i = PAIR ? 0 : s; i < n && ok; i += PAIR ? 1 : 2) {
         const int t = w.t0 + i;
