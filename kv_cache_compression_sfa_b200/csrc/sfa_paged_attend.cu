@@ -44,18 +44,23 @@ __device__ __forceinline__ void simt_load(const AttendParams& p, const AttendIte
   constexpr int EPC = 16 / static_cast<int>(sizeof(T));
   const T* kp = static_cast<const T*>(p.c.k_pages);
   const T* vp = static_cast<const T*>(p.c.v_pages);
-  for (int a = threadIdx.x; a < kSimtKeys * CH; a += kSimtThreads) {
-    const int row = a / CH, ch = a - row * CH;
+  constexpr int N = kSimtKeys * CH / kSimtThreads;  // chunks of a thread
+  long long off[N];  // -1: zeros; all page ids are asked for before the first copy
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int a = static_cast<int>(threadIdx.x) + i * kSimtThreads, row = a / CH, ch = a % CH;
     const int slot = tile * kSimtKeys + row;
-    long long off = 0;
-    bool in = slot < it.kv_end;
-    if (in) {
-      const int pg = page_of(p.c, it.b, slot);
-      in = pg >= 0;
-      if (in) off = page_base<D>(p.c, p.c.l0 + it.l, pg, it.kh) + static_cast<long long>(slot & (p.c.ps - 1)) * D + ch * EPC;
-    }
-    cp_async16_zfill(st + row * P::krow + ch * 16, kp + off, in);
-    cp_async16_zfill(st + P::kbytes + row * D * static_cast<int>(sizeof(T)) + ch * 16, vp + off, in);
+    const int pg = slot < it.kv_end ? page_of(p.c, it.b, slot) : -1;
+    off[i] = pg < 0 ? -1
+                    : page_base<D>(p.c, p.c.l0 + it.l, pg, it.kh) + static_cast<long long>(slot & (p.c.ps - 1)) * D + ch * EPC;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int a = static_cast<int>(threadIdx.x) + i * kSimtThreads, row = a / CH, ch = a % CH;
+    const bool in = off[i] >= 0;
+    const long long o = in ? off[i] : 0;
+    cp_async16_zfill(st + row * P::krow + ch * 16, kp + o, in);
+    cp_async16_zfill(st + P::kbytes + row * D * static_cast<int>(sizeof(T)) + ch * 16, vp + o, in);
   }
 }
 
@@ -130,22 +135,26 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attend_simt_kernel(const __gr
         }
       }
       const bool edge = (t + 1) * kSimtKeys > it.ctx;  // some key of the tile is not visible to all rows
+      if (edge) {
 #pragma unroll
-      for (int r = 0; r < RPW; ++r) {
-        if (edge) {
-          const int row = it.row0 + warp * RPW + r;
-          const int node = min(p.by_group(row), max(it.len - 1, 0));
+        for (int r = 0; r < RPW; ++r) {
+          const int node = min(p.by_group(it.row0 + warp * RPW + r), max(it.len - 1, 0));
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int rel = t * kSimtKeys + lane + 32 * u - it.ctx;
             if (rel >= 0 && !sees_new(p, it.b, node, it.len, rel)) s[r][u] = -INFINITY;
           }
         }
-        const float mn = fmaxf(m[r], warp_max(fmaxf(s[r][0], s[r][1])));
-        const float base = mn == -INFINITY ? 0.f : mn;
+      }
+      float mn[RPW];
+#pragma unroll
+      for (int r = 0; r < RPW; ++r) mn[r] = fmaxf(m[r], warp_max_redux(fmaxf(s[r][0], s[r][1])));
+#pragma unroll
+      for (int r = 0; r < RPW; ++r) {
+        const float base = mn[r] == -INFINITY ? 0.f : mn[r];
         const float fix = exp2_approx(m[r] - base);
         const float p0 = exp2_approx(s[r][0] - base), p1 = exp2_approx(s[r][1] - base);
-        m[r] = mn;
+        m[r] = mn[r];
         l[r] = fmaf(l[r], fix, p0 + p1);
 #pragma unroll
         for (int e = 0; e < DPL; ++e) o[r][e] *= fix;
@@ -153,7 +162,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attend_simt_kernel(const __gr
         s_p[(lane + 32) * RPW + r] = p1;
       }
       __syncwarp();
-#pragma unroll 2
+#pragma unroll 8
       for (int j = 0; j < kSimtKeys; ++j) {
         float v[DPL], w[RPW];
         VecLoad<T, DPL>::run(vs + j * D + lane * DPL, v);
