@@ -379,7 +379,11 @@ SFA_API int sfa_debug_set_paths(sfa_handle* h, int decode_tile, int prefill_near
  * as they are); a page id outside 0 .. n_pages - 1 that a token needs is not
  * written by append and accept, and reads as keys and values of zero in attend.
  * Two sequences may share pages that no call writes; a page written for one
- * sequence belongs to it alone. */
+ * sequence belongs to it alone.  Before any launch the calls return
+ * SFA_ERR_INVALID_ARG (a bad handle, layer range, size or NULL argument, or
+ * another device current than the handle's), SFA_ERR_ALIGNMENT or
+ * SFA_ERR_UNSUPPORTED (a page size other than those below, more pages, rows or
+ * tiles than stated); n_max == 0 enqueues nothing. */
 typedef struct sfa_kv_cache {
   void* k_pages;         /* DEVICE [n_layers][n_pages][n_kv][page_size][d] in_dtype       */
   void* v_pages;         /* DEVICE, same layout                                            */
@@ -450,7 +454,8 @@ SFA_API size_t sfa_kv_attend_workspace_bytes(const sfa_handle* h, int n_max);
  * with n_max > SFA_TREE_MAX, batch > 4096, layer_count * batch * n_max * n_q >
  * 2^31 - 1, or more than 2^30 tiles of 64 keys over all layers, sequences, KV
  * heads and row tiles at max_pages full pages.
- * SFA_ERR_WORKSPACE if workspace is too small. */
+ * SFA_ERR_WORKSPACE if workspace is too small.  A device-side wait that runs out
+ * is latched as SFA_ERR_DEVICE_TIMEOUT; that call's out is incomplete. */
 SFA_API int sfa_kv_attend(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begin, int layer_count,
                           const void* q, int n_max, const int* lens, const int* ctx_lens,
                           const uint32_t* mask, int batch, void* out, void* workspace,

@@ -765,7 +765,11 @@ class SfaPagedCache:
         need = self._ws_need.get(n)
         if need is None:
             need = self._ws_need[n] = sfa_kv_attend_workspace_bytes(self.handle, n)
-        key = _stream_ptr(stream)
+        if stream is None and 0 <= self._index != torch.cuda.current_device():
+            with torch.cuda.device(self._index):
+                key = _stream_ptr(None)
+        else:
+            key = _stream_ptr(stream)
         ws = self._ws.get(key)
         if ws is None or ws.numel() < need:
             if ws is not None and isinstance(stream, torch.cuda.Stream):

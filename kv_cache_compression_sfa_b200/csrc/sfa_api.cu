@@ -734,9 +734,9 @@ int sfa_tree_plan(const sfa_handle* h, const int* parents, int n_max, const int*
                   int batch, int* positions, uint32_t* mask, void* stream) {
   const int st = paged_status(h, n_max, ctx_lens, batch);
   if (st != SFA_OK) return st;
+  if (n_max == 0) return SFA_OK;
   if (!parents || (!positions && !mask)) return SFA_ERR_INVALID_ARG;
   if (n_max > SFA_TREE_MAX) return SFA_ERR_UNSUPPORTED;
-  if (n_max == 0) return SFA_OK;
   if (!on_device(h)) return SFA_ERR_INVALID_ARG;
   PlanParams p;
   p.parents = parents;
@@ -760,7 +760,7 @@ int sfa_kv_append(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begi
   std::memset(&p, 0, sizeof(p));
   st = fill_paged(p.c, h, cache, layer_begin, layer_count, n_max, lens, ctx_lens, batch);
   if (st != SFA_OK) return st;
-  if (!k || !v || (q == nullptr) != (q_out == nullptr)) return SFA_ERR_INVALID_ARG;
+  if (n_max > 0 && (!k || !v || (q == nullptr) != (q_out == nullptr))) return SFA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out))
     return SFA_ERR_ALIGNMENT;
   if (rope) {
@@ -847,9 +847,9 @@ int sfa_kv_accept(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begi
   std::memset(&p, 0, sizeof(p));
   st = fill_paged(p.c, h, cache, layer_begin, layer_count, n_max, nullptr, ctx_lens, batch);
   if (st != SFA_OK) return st;
+  if (n_max == 0) return SFA_OK;
   if (!path || !n_accept) return SFA_ERR_INVALID_ARG;
   if (n_max > SFA_TREE_MAX) return SFA_ERR_UNSUPPORTED;
-  if (n_max == 0) return SFA_OK;
   if (!on_device(h)) return SFA_ERR_INVALID_ARG;
   p.path = path;
   p.n_accept = n_accept;

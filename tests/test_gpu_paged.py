@@ -383,6 +383,142 @@ def test_attend_on_a_stream_and_in_a_graph():
         assert torch.equal(out[:, 0, :3], eager[:, 0, :3]) and torch.equal(out[:, 1, :2], eager[:, 1, :2])
 
 
+def test_attend_on_two_streams_at_once():
+    a = Case("qwen7b", "bf16", [3000, 20], [2, 1], 2, 16, seed=25)
+    b_q = torch.randn_like(a.q)
+    want = [a.cache.attend(0, q, a.ctx_d, lens=a.lens_d) for q in (a.q, b_q)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.zeros_like(want[0]) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, q, o in zip(streams, (a.q, b_q), outs):
+            a.cache.attend(0, q, a.ctx_d, lens=a.lens_d, out=o, stream=s)
+    torch.cuda.synchronize()
+    assert sfa.sfa_check_device_status(a.h) == sfa.SFA_OK
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
+def test_attend_shared_prefix_pages():
+    """Two sequences whose first pages are the same."""
+    c = Case("qwen05b", "bf16", [64, 64], [3, 3], 3, 16, seed=26)
+    c.table[1, :4] = c.table[0, :4]
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_nan_queries_reach_their_own_row_alone(dtype):
+    c = Case("qwen05b", dtype, [200, 9], [3, 3], 3, 16, seed=27)
+    clean = c.check()
+    c.q[0, 0, 1, 4] = float("nan")
+    out = c.cache.attend(0, c.q, c.ctx_d, lens=c.lens_d)
+    d = 64
+    assert torch.isnan(out[0, 0, 1, 4 * d:5 * d]).all()
+    out[0, 0, 1, 4 * d:5 * d] = clean[0, 0, 1, 4 * d:5 * d]
+    assert torch.equal(out, clean)
+
+
+# ---------------------------------------------------------------- refusals
+
+
+def test_calls_refuse_before_any_launch():
+    import ctypes
+    c = Case("qwen05b", "bf16", [5, 6], [2, 2], 2, 16, layers=2, seed=28)
+    lib, h = sfa.load_library(), c.h.ptr
+    P = lambda t: t.data_ptr()  # noqa: E731
+    ws = torch.empty(sfa.sfa_kv_attend_workspace_bytes(c.h, 2), dtype=torch.uint8, device="cuda")
+    out = torch.zeros(2, 2, 2, c.h.cfg.hidden, dtype=torch.bfloat16, device="cuda")
+    before = [t.clone() for t in (c.k_pages, c.v_pages, out)]
+
+    def cache(**kw):
+        x = dict(k_pages=P(c.k_pages), v_pages=P(c.v_pages), n_pages=c.k_pages.shape[1], page_size=16,
+                 max_pages=c.table.shape[1], page_table=P(c.table))
+        x.update(kw)
+        return ctypes.byref(sfa.sfa_kv_cache(*[x[f] for f, _ in sfa.sfa_kv_cache._fields_]))
+
+    def attend(cc=None, l0=0, lc=2, q=P(c.q), n=2, ctx=P(c.ctx_d), mask=None, B=2, o=P(out), w=P(ws), wb=ws.numel(), hh=h):
+        return lib.sfa_kv_attend(hh, cc or cache(), l0, lc, q, n, None, ctx, mask, B, o, w, wb, None)
+
+    def append(cc=None, l0=0, lc=2, q=P(c.q), k=P(c.k), v=P(c.v), n=2, rope=None, B=2, qo=P(c.q), ko=None):
+        return lib.sfa_kv_append(h, cc or cache(), l0, lc, q, k, v, n, None, P(c.ctx_d), None,
+                                 None if rope is None else ctypes.byref(rope.c), B, qo, ko, None)
+
+    def accept(cc=None, l0=0, lc=2, path=P(c.table), n=1, na=P(c.lens_d), B=2):
+        return lib.sfa_kv_accept(h, cc or cache(), l0, lc, path, n, na, P(c.ctx_d), B, None)
+
+    inv, ali, uns, wsp = sfa.SFA_ERR_INVALID_ARG, sfa.SFA_ERR_ALIGNMENT, sfa.SFA_ERR_UNSUPPORTED, sfa.SFA_ERR_WORKSPACE
+    for call in (attend, append, accept):
+        for kw in (dict(l0=-1), dict(l0=1), dict(lc=0), dict(lc=3), dict(l0=2 ** 31 - 1, lc=2), dict(n=-1), dict(B=0)):
+            assert call(**kw) == inv, (call, kw)
+        for kw in (dict(k_pages=None), dict(v_pages=None), dict(page_table=None), dict(page_size=0), dict(n_pages=0),
+                   dict(max_pages=0)):
+            assert call(cc=cache(**kw)) == inv, (call, kw)
+        assert call(cc=cache(k_pages=P(c.k_pages) + 8)) == ali
+        for kw in (dict(page_size=4), dict(page_size=24), dict(page_size=512), dict(n_pages=2 ** 31), dict(n_pages=2 ** 29),
+                   dict(max_pages=2 ** 27)):
+            assert call(cc=cache(**kw)) == uns, (call, kw)
+        assert call(n=0) == sfa.SFA_OK
+    assert attend(q=None) == inv and attend(o=None) == inv and attend(ctx=None) == inv and attend(hh=None) == inv
+    assert attend(q=P(c.q) + 2) == ali and attend(w=P(ws) + 4) == ali
+    assert attend(w=None) == wsp and attend(wb=ws.numel() - 1) == wsp
+    assert attend(n=1025, mask=P(c.table)) == uns and attend(B=4097) == uns and attend(n=2 ** 30) == uns
+    assert append(k=None) == inv and append(v=None) == inv and append(q=None) == inv and append(qo=None) == inv
+    assert append(ko=P(c.k) + 2) == ali and append(n=2 ** 30) == uns
+    for rope, code in ((sfa.SfaRope(style=2), inv), (sfa.SfaRope(dims=8), inv), (sfa.SfaRope(dims=80), inv),
+                       (sfa.SfaRope(base=0.0), inv), (sfa.SfaRope(base=float("inf")), inv),
+                       (sfa.SfaRope(inv_freq=[float("nan")] * 32), inv)):
+        assert append(rope=rope) == code
+    assert accept(path=None) == inv and accept(na=None) == inv and accept(n=1025) == uns
+    one = torch.zeros(2, 1025, dtype=torch.int32, device="cuda")
+    assert lib.sfa_tree_plan(h, P(one), 1025, None, P(c.ctx_d), 2, P(one), None, None) == uns
+    assert lib.sfa_tree_plan(h, P(one), 2, None, P(c.ctx_d), 2, None, None, None) == inv
+    assert lib.sfa_tree_plan(h, None, 2, None, P(c.ctx_d), 2, P(one), None, None) == inv
+    assert lib.sfa_tree_plan(h, P(one), 2, None, None, 2, P(one), None, None) == inv
+    assert sfa.sfa_kv_attend_workspace_bytes(c.h, 0) == 0
+    torch.cuda.synchronize()
+    assert sfa.sfa_check_device_status(c.h) == sfa.SFA_OK
+    assert all(torch.equal(a, b) for a, b in zip(before, (c.k_pages, c.v_pages, out)))
+
+
+def test_binding_refuses_and_takes_empty_calls():
+    c = Case("qwen05b", "bf16", [5, 6], [2, 2], 2, 16, seed=29)
+    with pytest.raises(ValueError):
+        c.cache.attend(0, c.q.float(), c.ctx_d)
+    with pytest.raises(ValueError):
+        c.cache.attend(0, c.q.cpu(), c.ctx_d)
+    with pytest.raises(ValueError):
+        c.cache.attend(0, c.q, c.ctx_d.cpu(), out=torch.zeros(1, 2, 2, 896, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        c.cache.append(0, c.q, c.k, c.v.transpose(3, 4), c.ctx_d, q_out=c.q)
+    with pytest.raises(ValueError):
+        c.cache.accept(0, 1, c.ctx_d[:, None].long(), c.lens_d, c.ctx_d)
+    with pytest.raises(sfa.SfaError):
+        c.cache.attend(1, c.q, c.ctx_d)
+    assert c.cache.attend(0, c.q[:, :, :0].contiguous(), c.ctx_d).shape == (1, 2, 0, 896)
+    c.cache.append(0, c.q[:, :, :0].contiguous(), c.k[:, :, :0].contiguous(), c.v[:, :, :0].contiguous(), c.ctx_d)
+    c.cache.accept(0, 1, torch.zeros(2, 0, dtype=torch.int32, device="cuda"), ints([0, 0]), c.ctx_d)
+    assert sfa.sfa_check_device_status(c.h) == sfa.SFA_OK
+
+
+@pytest.mark.skipif(sfa._fast is None, reason="the extension is not built")
+def test_extension_and_ctypes_paths_agree(monkeypatch):
+    c = Case("qwen05b", "bf16", [50, 6], [3, 2], 3, 16, seed=30)
+    rope = sfa.SfaRope()
+    runs = []
+    for fast in (True, False):
+        if not fast:
+            monkeypatch.setattr(sfa, "_fast", None)
+        cache = sfa.SfaPagedCache(c.h, c.k_pages.clone(), c.v_pages.clone(), c.table)
+        assert (cache._spec is not None) == fast
+        qo, out = torch.zeros_like(c.q), torch.zeros(1, 2, 3, 896, dtype=torch.bfloat16, device="cuda")
+        pos, mask = torch.zeros(2, 3, dtype=torch.int32, device="cuda"), torch.zeros(2, 3, 1, dtype=torch.int32, device="cuda")
+        sfa.sfa_tree_plan(c.h, ints([[-1, 0, 0], [-1, 0, 1]]), c.ctx_d, lens=c.lens_d, positions=pos, mask=mask)
+        cache.append(0, c.q, c.k, c.v, c.ctx_d, lens=c.lens_d, positions=pos, rope=rope, q_out=qo)
+        cache.attend(0, qo, c.ctx_d, lens=c.lens_d, mask=mask, out=out)
+        cache.accept(0, 1, ints([[0, 2, 0], [1, 0, 0]]), ints([2, 1]), c.ctx_d)
+        runs.append([pos, mask, qo, out, cache.k_pages, cache.v_pages])
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
 # ----------------------------------------------------------------- accept
 
 
@@ -413,6 +549,37 @@ def test_accept_skips_bad_paths():
     c.cache.accept(0, 1, ints([p + [0] * 3 for p in paths]), ints([3, 3, 3, 3, 7, 3]), ints([3, 3, 3, 3, 3, -2]))
     assert sfa.sfa_check_device_status(c.h) == sfa.SFA_ERR_INVALID_ARG
     assert torch.equal(c.k_pages, k0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_pages_whose_offsets_pass_32_bits(dtype):
+    """Page ids whose element offsets are above 2^31 (bytes above 2^32), in
+    every call."""
+    nq, nkv, d = SHAPES["qwen7b"]
+    h = handle("qwen7b", dtype)
+    page, n_pages = 256, 2 ** 31 // (nkv * 256 * d) + 40
+    k_pages, v_pages = (torch.empty(1, n_pages, nkv, page, d, device="cuda", dtype=DT[dtype]) for _ in range(2))
+    ids = [n_pages - 1, 3, n_pages - 30, n_pages - 7]
+    g = torch.Generator(device="cuda").manual_seed(33)
+    for p in ids:
+        k_pages[:, p].normal_(generator=g)
+        v_pages[:, p].normal_(generator=g)
+    low = [torch.stack([x[:, p] for p in ids], 1) for x in (k_pages, v_pages)]     # the same pages in a small cache
+    big = sfa.SfaPagedCache(h, k_pages, v_pages, ints([ids[:2], ids[2:]]))
+    small = sfa.SfaPagedCache(h, *low, ints([[0, 1], [2, 3]]))
+    q = torch.randn(1, 2, 5, nq, d, generator=g, device="cuda").to(DT[dtype])
+    k, v = (torch.randn(1, 2, 5, nkv, d, generator=g, device="cuda").to(DT[dtype]) for _ in range(2))
+    ctx = ints([300, 254])
+    outs = []
+    for c in (big, small):
+        qr, _ = c.append(0, q, k, v, ctx, rope=sfa.SfaRope())
+        out = c.attend(0, qr, ctx)
+        c.accept(0, 1, ints([[1, 3, 4, 0, 0], [0, 2, 4, 0, 0]]), ints([3, 3]), ctx)
+        outs.append((qr, out))
+    assert sfa.sfa_check_device_status(h) == sfa.SFA_OK
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    for x, y in ((k_pages, low[0]), (v_pages, low[1])):
+        assert all(torch.equal(x[:, p], y[:, i]) for i, p in enumerate(ids))
 
 
 # --------------------------------------------------------------- together
