@@ -315,6 +315,12 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
     mbar_fence_init();
   }
   if (warp == kTcMmaWarp) tmem_alloc(&sh.tmem, kTmemCols);
+  // Rows of q that no copy writes stay zero: their products cost the tensor
+  // cores less power, which sets the clock of a card that streams a cache
+  // (256 sequences of one token for seconds: 237 us with whatever lay there).
+  for (int i = tid; i < (PAIR ? 2 : 1) * P::tile / 16; i += kTcThreads)
+    reinterpret_cast<uint4*>(smem + P::q)[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();  // barriers and tensor memory are set up
   tc_fence_after();
@@ -324,6 +330,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
   const uint32_t tmem = sh.tmem;
   // up to 64 rows leave room for the next item's q behind this one's
   const int q_bufs = !PAIR && p.rows_step <= kTcRows / 2 ? 2 : 1;
+  const int q_next = (p.rows_step + 7) / 8 * 1024;
   const int tile_rows = PAIR ? p.rows_step / 2 : p.rows_step;  // rows of one row tile
   bool ok = true;
 
@@ -388,7 +395,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
           mbar_arrive_expect_tx(&bars.q_full[qb], static_cast<unsigned>(tile_rows * 128 * (D / 64) * (PAIR ? 2 : 1)));
           for (int s = 0; s < (PAIR ? 2 : 1); ++s)
             for (int h = 0; h < D / 64; ++h)
-              tma_load_4d(smem + P::q + s * P::tile + qb * (kTcRows / 2 * 128) + h * (kTcRows * 128), &maps.q, h * 64,
+              tma_load_4d(smem + P::q + s * P::tile + qb * q_next + h * (kTcRows * 128), &maps.q, h * 64,
                           w.it.kh * p.c.G, node0 + s * nb, w.it.l * p.c.B + w.it.b, &bars.q_full[qb]);
         }
         __syncwarp();
@@ -478,7 +485,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
         const int qb = n_q % q_bufs;
         if (!wait(&bars.q_full[qb], static_cast<unsigned>(n_q / q_bufs))) break;
         ++n_q;
-        const uint64_t d_qb = d_q + (qb * (kTcRows / 2 * 128) >> 4);
+        const uint64_t d_qb = d_q + (qb * q_next >> 4);
         int st_k = 0, st_v = 0;
         if (PAIR) {
           if (!next_kv(&st_k)) break;
@@ -630,7 +637,8 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
                 tmem_st32(t_o + c, reinterpret_cast<const uint32_t*>(o));
               }
             }
-            l += store_probs<HK>(x, p.scale_log2, m == -INFINITY ? 0.f : m, t_s);
+            // (rows that are not there get P = 0, as those of warps without rows have)
+            l += store_probs<HK>(x, p.scale_log2, r >= rows ? INFINITY : m == -INFINITY ? 0.f : m, t_s);
             tmem_st_wait();
           }
           tc_fence_before();
