@@ -331,6 +331,9 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
   // up to 64 rows leave room for the next item's q behind this one's
   const int q_bufs = !PAIR && p.rows_step <= kTcRows / 2 ? 2 : 1;
   const int q_next = (p.rows_step + 7) / 8 * 1024;
+  // and take products of 64 rows, whose rows lie in the first 16 lanes of every
+  // quarter of tensor memory
+  const bool m64 = q_bufs == 2;
   const int tile_rows = PAIR ? p.rows_step / 2 : p.rows_step;  // rows of one row tile
   bool ok = true;
 
@@ -426,8 +429,8 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
     // uniform; one elected lane issues.
     {
       const bool leader = elect_one();
-      const uint32_t idesc_qk = umma_idesc_bf16(kTcRows, HK, false);
-      const uint32_t idesc_pv = umma_idesc_bf16(kTcRows, D, true);
+      const uint32_t idesc_qk = umma_idesc_bf16(m64 ? 64 : kTcRows, HK, false);
+      const uint32_t idesc_pv = umma_idesc_bf16(m64 ? 64 : kTcRows, D, true);
       const uint64_t d_q = desc_sw128(smem_u32(smem + P::q), 16, 1024);
       const uint64_t d_k = desc_sw128(smem_u32(smem + P::ring), 16, 1024);
       const uint64_t d_v = desc_sw128(smem_u32(smem + P::ring), kTcKeys * 128, 1024);
@@ -553,7 +556,8 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
     if constexpr (PAIR) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTcSoftmaxRegs));
     // ---- softmax of stream s, a thread per row
     const int s = warp >> 2, sub = warp & 3;
-    const int r = sub * 32 + lane;  // row of the tile, tensor-memory lane
+    const int tl = sub * 32 + lane;  // tensor-memory lane
+    const int r = !m64 ? tl : lane < 16 ? sub * 16 + lane : kTcRows;  // its row of the tile
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(sub * 32) << 16);
     const uint32_t t_o = lane_base + 256u + static_cast<uint32_t>(s) * D;
     unsigned n_t = 0, n_o = 0, n_piece = 0;  // tiles and steps of this stream, and pieces, so far
@@ -565,7 +569,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       const int n = w.t1 - w.t0;
       const int row0 = it.row0 + (PAIR ? s * tile_rows : 0);
       const int rows = min(tile_rows, it.rows - (PAIR ? s * tile_rows : 0));  // <= 0: an empty second tile
-      const bool warp_live = sub * 32 < rows;
+      const bool warp_live = sub * (m64 ? 16 : 32) < rows;
       const int nd = p.by_group(row0 + r), node = min(nd, max(it.len - 1, 0));
       // keys below this are visible to every row of the piece
       const int full_end = p.mask ? it.ctx : it.ctx + p.by_group(it.row0) + 1;
@@ -580,7 +584,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
           ok = mbar_wait_bounded(&bars.kv_full[st], (at / NS) & 1u, kTcPollLimit, p.c.err);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          clean_values<D>(smem + P::ring + st * P::tile, full_end - t * kTcKeys, it.kv_end - t * kTcKeys, r, &sh.bad[s]);
+          clean_values<D>(smem + P::ring + st * P::tile, full_end - t * kTcKeys, it.kv_end - t * kTcKeys, tl, &sh.bad[s]);
         }
 #pragma unroll 1
         for (int h = 0; h < NH; ++h) {
@@ -656,14 +660,14 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       ++n_piece;
       ok = __all_sync(0xffffffffu, ok);
       if (!PAIR) {
-        sh.ml[s][r] = make_float2(m, l);
+        sh.ml[s][tl] = make_float2(m, l);
         named_bar_sync(1, kTcSoftmaxThreads);
       }
       if (ok) {
         tc_fence_after();
         float w0 = 1.f, w1 = 0.f;
         if (!PAIR) {
-          const float2 a = sh.ml[0][r], b = sh.ml[1][r];
+          const float2 a = sh.ml[0][tl], b = sh.ml[1][tl];
           m = fmaxf(a.x, b.x);
           const float base = m == -INFINITY ? 0.f : m;
           w0 = exp2_approx(a.x - base);
