@@ -80,7 +80,7 @@ struct TcBars {
 struct TcShared {
   TcBars bars;
   float2 ml[2][kTcRows];  // maximum and sum of both streams' rows
-  int bad[2];             // clean_values found elements that are not finite
+  int bad[2][2];          // [piece & 1][stream]: clean_values found elements that are not finite
   uint32_t tmem;
 };
 
@@ -282,9 +282,15 @@ __device__ __forceinline__ void add_nonfinite(const AttendParams& p, const Atten
   }
 }
 
-template <int D, bool PAIR>
+// Kernels by the rows of a call: up to 64 (products of 64 rows), one row tile, or
+// pairs of row tiles.  Each has its code alone: a switch at run time between the
+// ways out of the first two cost a call of one token 0.6 us.
+enum TcMode { kFew = 0, kOne = 1, kPair = 2 };
+
+template <int D, int MODE>
 __global__ void __launch_bounds__(kTcThreads, 1)
 attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ TcMaps maps) {
+  constexpr bool PAIR = MODE == kPair, m64 = MODE == kFew;
   using P = TcPlan<D, PAIR>;
   constexpr int NS = P::stages, HK = P::step, NH = P::steps;
   // the kernel has no other shared memory: the dynamic block starts on the 1024
@@ -309,7 +315,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       }
       mbar_init(&bars.o_step[s], 1);
       mbar_init(&bars.o_done[s], 1);
-      sh.bad[s] = 0;
+      sh.bad[0][s] = sh.bad[1][s] = 0;
     }
     mbar_init(&bars.drain, 1);
     mbar_fence_init();
@@ -328,12 +334,11 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
   pdl_wait();
   const AttendRun run = find_run(p, blockIdx.x == 0 && warp == 0);
   const uint32_t tmem = sh.tmem;
-  // up to 64 rows leave room for the next item's q behind this one's
-  const int q_bufs = !PAIR && p.rows_step <= kTcRows / 2 ? 2 : 1;
-  const int q_next = (p.rows_step + 7) / 8 * 1024;
-  // and take products of 64 rows, whose rows lie in the first 16 lanes of every
-  // quarter of tensor memory
-  const bool m64 = q_bufs == 2;
+  // Up to 64 rows leave room for the next item's q behind this one's, and take
+  // products of 64 rows, whose rows lie in the first 16 lanes of every quarter
+  // of tensor memory.
+  constexpr int q_bufs = m64 ? 2 : 1;
+  const int q_next = m64 ? (p.rows_step + 7) / 8 * 1024 : 0;
   const int tile_rows = PAIR ? p.rows_step / 2 : p.rows_step;  // rows of one row tile
   bool ok = true;
 
@@ -510,8 +515,10 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
             if (!ok) break;
             ++n_p[0];
             ++n_p[1];
-            commit(&bars.kv_empty[st_v]);
-            if (more) commit(&bars.kv_empty[st_k]);
+            if (more) {  // (the piece's last values' buffer is the softmax's, for its result)
+              commit(&bars.kv_empty[st_v]);
+              commit(&bars.kv_empty[st_k]);
+            }
             if (i + 2 == n) commit(&bars.q_empty[qb]);
             if (!more)
               for (int s = 0; s < 2; ++s) commit(&bars.o_done[s]);
@@ -536,7 +543,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
             }
             if (!ok) break;
             ++n_p[s];
-            commit(&bars.kv_empty[st_v]);
+            if (i + 1 < n || m64) commit(&bars.kv_empty[st_v]);  // (the last one is the softmax's, for its result)
             if (more) commit(&bars.kv_empty[st_k]);
             if (i + 3 == n) commit(&bars.q_empty[qb]);
           }
@@ -577,15 +584,6 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       for (int i = PAIR ? 0 : s; i < n && ok; i += PAIR ? 1 : 2) {
         const int t = w.t0 + i;
         const bool masked = (t + 1) * kTcKeys > full_end;
-        if (masked && (!PAIR || s == 0)) {
-          // this tile's values: their buffer's place in the loader's order
-          const unsigned at = n_kv + static_cast<unsigned>(PAIR ? 2 * i + 1 : (n == 1 ? 1 : min(2 * i + 2, n + i)));
-          const unsigned st = at % NS;
-          ok = mbar_wait_bounded(&bars.kv_full[st], (at / NS) & 1u, kTcPollLimit, p.c.err);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          clean_values<D>(smem + P::ring + st * P::tile, full_end - t * kTcKeys, it.kv_end - t * kTcKeys, tl, &sh.bad[s]);
-        }
 #pragma unroll 1
         for (int h = 0; h < NH; ++h) {
           const bool first = h == 0 && (PAIR ? i == 0 : i < 2);
@@ -594,6 +592,18 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
           ok = mbar_wait_bounded(&bars.s_full[s][h], n_t & 1u, kTcPollLimit, p.c.err);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
+          if (masked && h == 0 && (!PAIR || s == 0)) {
+            // This tile's values: their buffer's place in the loaders' order.  The
+            // scores came after the values before the last were used, so the
+            // buffer's phase can be told from its last but one.
+            const unsigned at = n_kv + static_cast<unsigned>(PAIR ? 2 * i + 1 : (n == 1 ? 1 : min(2 * i + 2, n + i)));
+            const unsigned st = at % NS;
+            ok = mbar_wait_bounded(&bars.kv_full[st], (at / NS) & 1u, kTcPollLimit, p.c.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            clean_values<D>(smem + P::ring + st * P::tile, full_end - t * kTcKeys, it.kv_end - t * kTcKeys, tl,
+                            &sh.bad[n_piece & 1u][s]);
+          }
           tc_fence_after();
           if (warp_live) {
             const uint32_t t_s = lane_base + static_cast<uint32_t>(s * kTcKeys + h * HK);
@@ -657,12 +667,12 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       // ---- result of the piece
       const bool starts = w.t0 == 0, whole = starts && w.t1 == it.nt;
       ok = ok && mbar_wait_bounded(&bars.o_done[PAIR ? s : 0], n_piece & 1u, kTcPollLimit, p.c.err);
-      ++n_piece;
       ok = __all_sync(0xffffffffu, ok);
       if (!PAIR) {
         sh.ml[s][tl] = make_float2(m, l);
         named_bar_sync(1, kTcSoftmaxThreads);
       }
+      const unsigned st_last = (n_kv - 1u) % NS;  // the last values: used up, and not given back yet
       if (ok) {
         tc_fence_after();
         float w0 = 1.f, w1 = 0.f;
@@ -674,48 +684,87 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
           w1 = exp2_approx(b.x - base);
           l = a.y * w0 + b.y * w1;
         }
-        const int bad = PAIR ? sh.bad[0] : sh.bad[0] | sh.bad[1];
-        const int slot0 = max(w.t0 * kTcKeys, full_end);
-        const int slot1 = min(w.t1 * kTcKeys, it.kv_end);
+        const int* bad = sh.bad[n_piece & 1u];
+        const bool fix = PAIR ? bad[0] != 0 : (bad[0] | bad[1]) != 0;
         const float inv = l == 0.f ? 0.f : 1.0f / l;
-        const int g = row0 + r - nd * p.c.G;
-        constexpr int NC = PAIR ? D : D / 2;  // columns of this warp group
-        constexpr int W = NC < 64 ? NC : 64;  // columns at a time
+        constexpr int NC = PAIR ? D : D / 2;       // columns of this warp group
+        constexpr int RB = P::tile / 8 / 32;       // bytes of a row in a warp's share of the buffer
+        constexpr int CH = RB / 16, W = RB / 2;    // 16-byte chunks of it; columns at a time
         const int c0 = PAIR ? 0 : s * NC;
-        const int rr = r + (PAIR ? s * tile_rows : 0);
+        const int row_w = sub * (m64 ? 16 : 32);   // the warp's first row, and its rows
+        const int rows_w = min(m64 ? 16 : 32, rows - row_w);
         const long long slot_row =
-            static_cast<long long>(piece_slot(static_cast<int>(blockIdx.x), starts)) * p.rows_step + rr;
+            static_cast<long long>(piece_slot(static_cast<int>(blockIdx.x), starts)) * p.rows_step + (PAIR ? s * tile_rows : 0);
+        const long long out_row = static_cast<long long>(it.l) * p.c.B + it.b;
         if (!whole && r < rows && c0 == 0)
-          *reinterpret_cast<float2*>(p.part_ml + slot_row * 2) = make_float2(m, l);
+          *reinterpret_cast<float2*>(p.part_ml + (slot_row + r) * 2) = make_float2(m, l);
+        // More than 64 rows go out through shared memory, so that a store covers
+        // whole lines (a row per lane touches 32 lines with every 16 bytes: a call
+        // of 64 new tokens took 29 us and takes 27); fewer go out from registers,
+        // which is 0.5 us sooner for a handful.
+        unsigned char* stage = smem + P::ring + st_last * P::tile + warp * (P::tile / 8);
+        auto chunk = [&](int row, int c) {  // conflict-free both ways
+          return reinterpret_cast<uint4*>(stage + row * RB + ((c ^ (CH == 8 ? row & 7 : (row >> 1) & 3)) << 4));
+        };
+        auto flush = [&](unsigned char* base, bool token_rows, long long pitch) {
+          __syncwarp();
+#pragma unroll 4
+          for (int k = 0; k < rows_w; k += 32 / CH) {
+            const int row = k + lane / CH;
+            if (row >= rows_w) break;
+            long long at = row_w + row;
+            if (token_rows) {
+              const int gr = row0 + row_w + row, node_r = p.by_group(gr);
+              at = (out_row * p.c.n_max + node_r) * p.c.nq + it.kh * p.c.G + (gr - node_r * p.c.G);
+            }
+            *reinterpret_cast<uint4*>(base + at * pitch + (lane % CH) * 16) = *chunk(row, lane % CH);
+          }
+          __syncwarp();
+        };
         if (warp_live) {
 #pragma unroll 1
           for (int c = 0; c < NC; c += W) {
             float o[W];
-            if (PAIR) {
+            const uint32_t t_c = lane_base + 256u + (PAIR ? s * D : c0) + c;
 #pragma unroll
-              for (int j = 0; j < W; j += 32) tmem_ld32_async(t_o + c + j, o + j);
+            for (int j = 0; j < W; j += 32) tmem_ld32_async(t_c + j, o + j);
+            if (!PAIR && n > 1) {
+              float o1[W];
+#pragma unroll
+              for (int j = 0; j < W; j += 32) tmem_ld32_async(t_c + D + j, o1 + j);
               tmem_ld_wait<W>(o);
+              tmem_ld_wait<W>(o1);
+#pragma unroll
+              for (int j = 0; j < W; ++j) o[j] = fmaf(o1[j], w1, o[j] * w0);
             } else {
-#pragma unroll
-              for (int j = 0; j < W; j += 32) tmem_ld32_async(lane_base + 256u + c0 + c + j, o + j);
-              if (n > 1) {
-                float o1[W];
-#pragma unroll
-                for (int j = 0; j < W; j += 32) tmem_ld32_async(lane_base + 256u + D + c0 + c + j, o1 + j);
-                tmem_ld_wait<W>(o);
-                tmem_ld_wait<W>(o1);
-#pragma unroll
-                for (int j = 0; j < W; ++j) o[j] = fmaf(o1[j], w1, o[j] * w0);
-              } else {
-                tmem_ld_wait<W>(o);
-              }
+              tmem_ld_wait<W>(o);
             }
-            if (r < rows) {
-              if (bad) add_nonfinite<W>(p, it, node, slot0, slot1, D, c0 + c, o);
-              if (whole) {
-                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
-                                     (((static_cast<long long>(it.l) * p.c.B + it.b) * p.c.n_max + nd) * p.c.nq +
-                                      it.kh * p.c.G + g) * D + c0 + c;
+            if (fix && r < rows)
+              add_nonfinite<W>(p, it, node, max(w.t0 * kTcKeys, full_end), min(w.t1 * kTcKeys, it.kv_end), D, c0 + c, o);
+            if (m64) {
+              if (r < rows) {
+                if (whole) {
+                  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
+                                       ((out_row * p.c.n_max + nd) * p.c.nq + it.kh * p.c.G + (row0 + r - nd * p.c.G)) * D + c0 + c;
+#pragma unroll
+                  for (int j = 0; j < W; j += 8) {
+                    uint32_t u[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                      const __nv_bfloat162 b = __floats2bfloat162_rn(o[j + 2 * e] * inv, o[j + 2 * e + 1] * inv);
+                      u[e] = *reinterpret_cast<const uint32_t*>(&b);
+                    }
+                    *reinterpret_cast<uint4*>(dst + j) = make_uint4(u[0], u[1], u[2], u[3]);
+                  }
+                } else {
+#pragma unroll
+                  for (int j = 0; j < W; j += 4)
+                    *reinterpret_cast<float4*>(p.part_o + (slot_row + r) * D + c0 + c + j) =
+                        make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                }
+              }
+            } else if (whole) {
+              if (r < rows) {
 #pragma unroll
                 for (int j = 0; j < W; j += 8) {
                   uint32_t u[4];
@@ -725,13 +774,19 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
                     const __nv_bfloat162 b = __floats2bfloat162_rn(o[j + 2 * e] * inv, o[j + 2 * e + 1] * inv);
                     u[e] = *reinterpret_cast<const uint32_t*>(&b);
                   }
-                  *reinterpret_cast<uint4*>(dst + j) = make_uint4(u[0], u[1], u[2], u[3]);
+                  *chunk(r - row_w, j / 8) = make_uint4(u[0], u[1], u[2], u[3]);
                 }
-              } else {
-                float* dst = p.part_o + slot_row * D + c0 + c;
+              }
+              flush(reinterpret_cast<unsigned char*>(p.out) + (c0 + c) * 2, true, D * 2);
+            } else {
 #pragma unroll
-                for (int j = 0; j < W; j += 4)
-                  *reinterpret_cast<float4*>(dst + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+              for (int q = 0; q < W; q += W / 2) {
+                if (r < rows)
+#pragma unroll
+                  for (int j = 0; j < W / 2; j += 4)
+                    *chunk(r - row_w, j / 4) = make_uint4(__float_as_uint(o[q + j]), __float_as_uint(o[q + j + 1]),
+                                                          __float_as_uint(o[q + j + 2]), __float_as_uint(o[q + j + 3]));
+                flush(reinterpret_cast<unsigned char*>(p.part_o) + slot_row * D * 4 + (c0 + c + q) * 4, false, D * 4);
               }
             }
           }
@@ -742,10 +797,14 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
         }
         tc_fence_before();
       }
-      // outputs and flags are read: the next piece may overwrite them
+      // outputs, flags and the buffer are read: the next piece may overwrite them
+      if (!m64) fence_proxy_async_smem();
       named_bar_sync(1, kTcSoftmaxThreads);
-      if (tid == 0) sh.bad[0] = sh.bad[1] = 0;
-      named_bar_sync(1, kTcSoftmaxThreads);
+      if (tid == 0) {
+        sh.bad[n_piece & 1u][0] = sh.bad[n_piece & 1u][1] = 0;
+        if (!m64) mbar_arrive(&bars.kv_empty[st_last]);
+      }
+      ++n_piece;
     }
     if (!wrote && tid == 0) write_meta(p, run, false, run.it, 0);
   }
@@ -799,31 +858,31 @@ cudaError_t encode_maps(const AttendParams& p, int D, int nodes, TcMaps* m) {
   return kv(&m->k, c.k_pages) && kv(&m->v, c.v_pages) ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, bool PAIR>
-constexpr int tc_smem() { return TcPlan<D, PAIR>::shared + static_cast<int>(sizeof(TcShared)); }
+template <int D, int MODE>
+constexpr int tc_smem() { return TcPlan<D, MODE == kPair>::shared + static_cast<int>(sizeof(TcShared)); }
 
-template <int D, bool PAIR>
+template <int D, int MODE>
 cudaError_t launch_tc(const AttendParams& p, cudaStream_t s) {
   TcMaps maps;
-  const cudaError_t e = encode_maps(p, D, p.rows_step / (PAIR ? 2 : 1) / p.c.G, &maps);
+  const cudaError_t e = encode_maps(p, D, p.rows_step / (MODE == kPair ? 2 : 1) / p.c.G, &maps);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.n_cta), 1, 1);
   cfg.blockDim = dim3(kTcThreads, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(tc_smem<D, PAIR>());
+  cfg.dynamicSmemBytes = static_cast<size_t>(tc_smem<D, MODE>());
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_tc_kernel<D, PAIR>, p, maps);
+  return cudaLaunchKernelEx(&cfg, attend_tc_kernel<D, MODE>, p, maps);
 }
 
-template <int D, bool PAIR>
+template <int D, int MODE>
 cudaError_t allow_tc() {
-  return cudaFuncSetAttribute(attend_tc_kernel<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              tc_smem<D, PAIR>());
+  return cudaFuncSetAttribute(attend_tc_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              tc_smem<D, MODE>());
 }
 
 }  // namespace
@@ -837,17 +896,20 @@ void attend_tc_rows(int G, int n_max, int* rows_step, int* kt) {
 }
 
 cudaError_t attend_tc_prepare() {
-  cudaError_t e = allow_tc<64, false>();
-  if (e == cudaSuccess) e = allow_tc<64, true>();
-  if (e == cudaSuccess) e = allow_tc<128, false>();
-  if (e == cudaSuccess) e = allow_tc<128, true>();
+  cudaError_t e = allow_tc<64, kFew>();
+  if (e == cudaSuccess) e = allow_tc<64, kOne>();
+  if (e == cudaSuccess) e = allow_tc<64, kPair>();
+  if (e == cudaSuccess) e = allow_tc<128, kFew>();
+  if (e == cudaSuccess) e = allow_tc<128, kOne>();
+  if (e == cudaSuccess) e = allow_tc<128, kPair>();
   return e;
 }
 
 cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, cudaStream_t s) {
-  const bool pair = p.c.n_max > kTcRows / p.c.G;
-  if (head_dim == 64) return pair ? launch_tc<64, true>(p, s) : launch_tc<64, false>(p, s);
-  return pair ? launch_tc<128, true>(p, s) : launch_tc<128, false>(p, s);
+  const int mode = p.c.n_max > kTcRows / p.c.G ? kPair : p.rows_step > kTcRows / 2 ? kOne : kFew;
+  if (head_dim == 64)
+    return mode == kPair ? launch_tc<64, kPair>(p, s) : mode == kOne ? launch_tc<64, kOne>(p, s) : launch_tc<64, kFew>(p, s);
+  return mode == kPair ? launch_tc<128, kPair>(p, s) : mode == kOne ? launch_tc<128, kOne>(p, s) : launch_tc<128, kFew>(p, s);
 }
 
 }  // namespace sfa
