@@ -656,3 +656,18 @@ def test_drafted_step_as_it_is_used(dtype):
         # the enhancement from two runs (the operator's tolerance each) and one rounding
         tol = (2e-3 if dtype == "bf16" else 1e-4) * (1 + x[:, b, :m].abs().double()) * 2 + ref.HALF[T] * want.abs()
         assert bool(((total[:, b, :m].double() - want).abs() <= tol).all())
+
+
+def test_few_and_many_results_agree():
+    """The same sequence in a call of few values (P in two parts) and in one of
+    many: both within their bounds, and the former nearer."""
+    c = Case("qwen05b", "bf16", [700] * 40, [1] * 40, 1, 16, seed=34)
+    many = c.check()
+    k = {}
+    for b in (0, 17):
+        one = sfa.SfaPagedCache(c.h, c.k_pages, c.v_pages, c.table[b:b + 1].contiguous())
+        k[b] = one.attend(0, c.q[:, b:b + 1].contiguous(), c.ctx_d[b:b + 1].contiguous())
+    r, bound = ref.attend(c.q.cpu(), c.k_pages.cpu(), c.v_pages.cpu(), c.table.cpu(), c.ctx, c.lens, lambda b, i: None)
+    for b, out in k.items():
+        ref.assert_within(out, r[:, b:b + 1], bound[:, b:b + 1] / 2, "few")   # without the rounding of P
+        assert float((out.double().cpu() - r[:, b:b + 1]).norm()) <= float((many[:, b:b + 1].double().cpu() - r[:, b:b + 1]).norm())
