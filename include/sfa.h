@@ -389,7 +389,7 @@ typedef struct sfa_kv_cache {
   void* v_pages;         /* DEVICE, same layout                                            */
   long long n_pages;     /* pages of a layer, n_layers * n_pages * n_kv <= 2^31 - 1        */
   int page_size;         /* tokens of a page: 8, 16, 32, 64, 128 or 256                    */
-  int max_pages;         /* entries of a row of page_table                                 */
+  int max_pages;         /* entries of a row of page_table, max_pages * page_size <= 2^30  */
   const int* page_table; /* DEVICE [batch][max_pages]; entries past a sequence's tokens are
                             not read                                                       */
 } sfa_kv_cache;

@@ -229,6 +229,7 @@ int prefill_impl(const sfa_handle* h, int layer_begin, int layer_count, const vo
 // ---- paged key/value cache: checks shared by its calls
 
 constexpr int kMaxPageSize = 256;
+constexpr long long kMaxSlots = 1LL << 30;  // of a sequence: slots and tile ends fit 32 bits
 
 // The current device must be the handle's: its kernels' attributes, error word
 // and SM count belong there.
@@ -256,7 +257,7 @@ int fill_paged(PagedParams& c, const sfa_handle* h, const sfa_kv_cache* cache, i
   if (ps < 8 || ps > kMaxPageSize || (ps & (ps - 1)) != 0) return SFA_ERR_UNSUPPORTED;
   if (cache->n_pages > 0x7fffffffLL ||
       cache->n_pages * h->cfg.n_layers > 0x7fffffffLL / h->cfg.n_kv_heads ||
-      static_cast<long long>(cache->max_pages) * ps > 0x7fffffffLL)
+      static_cast<long long>(cache->max_pages) * ps > kMaxSlots)
     return SFA_ERR_UNSUPPORTED;
   if (static_cast<long long>(layer_count) * batch > 0x7fffffffLL) return SFA_ERR_UNSUPPORTED;
   c.k_pages = cache->k_pages;

@@ -72,7 +72,7 @@ struct TcMaps {
 struct TcBars {
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[12], kv_empty[12];
-  uint64_t s_full[2][2], p_full[2][2];  // [stream][half]
+  uint64_t s_full[2][2], p_full[2][2];  // [stream][step]
   uint64_t o_step[2];                   // a step is added to the stream's output
   uint64_t o_done[2], drain;            // the piece's last one (PAIR: of each stream, else of both)
 };

@@ -454,7 +454,7 @@ def test_calls_refuse_before_any_launch():
             assert call(cc=cache(**kw)) == inv, (call, kw)
         assert call(cc=cache(k_pages=P(c.k_pages) + 8)) == ali
         for kw in (dict(page_size=4), dict(page_size=24), dict(page_size=512), dict(n_pages=2 ** 31), dict(n_pages=2 ** 29),
-                   dict(max_pages=2 ** 27)):
+                   dict(max_pages=2 ** 26 + 1)):
             assert call(cc=cache(**kw)) == uns, (call, kw)
         assert call(n=0) == sfa.SFA_OK
     assert attend(q=None) == inv and attend(o=None) == inv and attend(ctx=None) == inv and attend(hh=None) == inv
