@@ -456,7 +456,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       int ring_st = 0;
       unsigned ring_turn = 0;
       int n_q = 0;
-      unsigned n_p[2] = {0u, 0u};
+      unsigned n_p[2][2] = {{0u, 0u}, {0u, 0u}};  // [stream][step]: how often its P was waited for
       auto wait = [&](uint64_t* bar, unsigned parity) {
         ok = ok && mbar_wait_bounded(bar, parity & 1u, kTcPollLimit, p.c.err);
         ok = __all_sync(0xffffffffu, ok);  // no lane may fall two phases behind
@@ -526,14 +526,12 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
 #pragma unroll
             for (int hs = 0; hs < 2 * NH; ++hs) {  // a step of both streams, then the next
               const int h = hs >> 1, s = hs & 1;
-              if (!wait(&bars.p_full[s][h], n_p[s])) continue;
+              if (!wait(&bars.p_full[s][h], n_p[s][h]++)) continue;
               pv(s, h, st_v, i == 0 && h == 0);
               if (more && hs == 0 && !next_kv(&st_k)) continue;
               if (more) qk(s, h, st_k, d_qb);
             }
             if (!ok) break;
-            ++n_p[0];
-            ++n_p[1];
             if (more) {  // (the piece's last values' buffer is the softmax's, for its result)
               commit(&bars.kv_empty[st_v]);
               commit(&bars.kv_empty[st_k]);
@@ -542,26 +540,39 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
             if (!more)
               for (int s = 0; s < 2; ++s) commit(&bars.o_done[s]);
           }
+        } else if (n == 1) {
+          // one tile: a half for each stream
+          if (!next_kv(&st_k)) break;
+          qk(0, 0, st_k, d_qb);
+          qk(1, 1, st_k, d_qb);
+          commit(&bars.kv_empty[st_k]);
+          commit(&bars.q_empty[qb]);
+          if (!next_kv(&st_v)) break;
+          if (!wait(&bars.p_full[0][0], n_p[0][0]++)) break;
+          pv(0, 0, st_v, true);
+          if (!wait(&bars.p_full[1][1], n_p[1][1]++)) break;
+          pv(1, 1, st_v, true);
+          if (m64) commit(&bars.kv_empty[st_v]);
+          commit(&bars.o_done[0]);
         } else {
-          for (int i = 0; i < min(n, 2) && ok; ++i) {
+          for (int i = 0; i < 2 && ok; ++i) {
             if (!next_kv(&st_k)) break;
             for (int h = 0; h < NH; ++h) qk(i, h, st_k, d_qb);
             commit(&bars.kv_empty[st_k]);
           }
           if (!ok) break;
-          if (n <= 2) commit(&bars.q_empty[qb]);
+          if (n == 2) commit(&bars.q_empty[qb]);
           for (int i = 0; i < n && ok; ++i) {
             const int s = i & 1;
             const bool more = i + 2 < n;
             if (!next_kv(&st_v)) break;
             for (int h = 0; h < NH && ok; ++h) {
-              if (!wait(&bars.p_full[s][h], n_p[s])) break;
+              if (!wait(&bars.p_full[s][h], n_p[s][h]++)) break;
               pv(s, h, st_v, i < 2 && h == 0);
               if (more && h == 0 && !next_kv(&st_k)) break;
               if (more) qk(s, h, st_k, d_qb);
             }
             if (!ok) break;
-            ++n_p[s];
             if (i + 1 < n || m64) commit(&bars.kv_empty[st_v]);  // (the last one is the softmax's, for its result)
             if (more) commit(&bars.kv_empty[st_k]);
             if (i + 3 == n) commit(&bars.q_empty[qb]);
@@ -586,7 +597,8 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
     const int r = !m64 ? tl : lane < 16 ? sub * 16 + lane : kTcRows;  // its row of the tile
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(sub * 32) << 16);
     const uint32_t t_o = lane_base + 256u + static_cast<uint32_t>(s) * D;
-    unsigned n_t = 0, n_o = 0, n_piece = 0;  // tiles and steps of this stream, and pieces, so far
+    unsigned n_s[2] = {0u, 0u};      // scores of each step's columns so far
+    unsigned n_o = 0, n_piece = 0;   // steps of this stream, and pieces, so far
     unsigned n_kv = 0;  // ring position of the piece's first buffer
     bool wrote = false;
     // after a wait that ran out a warp only keeps the CTA's barriers company
@@ -600,18 +612,21 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       // keys below this are visible to every row of the piece
       const int full_end = p.mask ? it.ctx : it.ctx + p.by_group(it.row0) + 1;
       float m = -INFINITY, l = 0.f;
-      for (int i = PAIR ? 0 : s; i < n && ok; i += PAIR ? 1 : 2) {
+      const bool halves = !PAIR && n == 1;  // one tile: stream s takes its half s
+      for (int i = PAIR || halves ? 0 : s; i < n && ok; i += PAIR ? 1 : 2) {
         const int t = w.t0 + i;
         const bool masked = (t + 1) * kTcKeys > full_end;
 #pragma unroll 1
         for (int h = 0; h < NH; ++h) {
-          const bool first = h == 0 && (PAIR ? i == 0 : i < 2);
+          if (halves && h != s) continue;
+          const bool first = halves || (h == 0 && (PAIR ? i == 0 : i < 2));
           RowMask<HK> vis;
           if (masked) vis = row_mask<HK>(p, it, node, t * kTcKeys + h * HK);
-          ok = mbar_wait_bounded(&bars.s_full[s][h], n_t & 1u, kTcPollLimit, p.c.err);
+          ok = mbar_wait_bounded(&bars.s_full[s][h], (h == 0 ? n_s[0] : n_s[1]) & 1u, kTcPollLimit, p.c.err);
+          h == 0 ? ++n_s[0] : ++n_s[1];
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (masked && h == 0 && (!PAIR || s == 0)) {
+          if (masked && h == 0 && (!PAIR || s == 0)) {  // (a tile in halves: by stream 0, whose product comes first)
             // This tile's values: their buffer's place in the loaders' order.  The
             // scores came after the values before the last were used, so the
             // buffer's phase can be told from its last but one.
@@ -680,7 +695,6 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
           ++n_o;
         }
         if (!ok) break;
-        ++n_t;
       }
       n_kv += 2u * static_cast<unsigned>(n);
       // ---- result of the piece
@@ -747,7 +761,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
             const uint32_t t_c = lane_base + 256u + (PAIR ? s * D : c0) + c;
 #pragma unroll
             for (int j = 0; j < W; j += 32) tmem_ld32_async(t_c + j, o + j);
-            if (!PAIR && n > 1) {
+            if constexpr (!PAIR) {
               float o1[W];
 #pragma unroll
               for (int j = 0; j < W; j += 32) tmem_ld32_async(t_c + D + j, o1 + j);

@@ -4,7 +4,8 @@
 A CTA walks pieces of 1 .. n key tiles.  Its roles: a warp that loads keys and
 q, a warp that loads values, a warp that issues the products, and four warps
 per stream for the softmax.  With PAIR both streams take every tile in one
-step; without, they take the tiles in turn, in two steps each.
+step; without, they take the tiles in turn, in two steps each, or a step each of
+an only tile.
 
 Each role is a generator that waits and arrives in the kernel's order.  A wait
 passes as the hardware's parity wait does.  Random interleavings must finish,
@@ -32,6 +33,7 @@ class _Bar:
 
 def _roles(pieces, pair, ns, q_bufs, rng, epilogue="o_done", clean_first=False):
     steps = 1 if pair else 2
+    few = not pair and q_bufs == 2  # up to 64 rows: results leave from registers
     B = {}
 
     def bar(*key, count=1):
@@ -67,7 +69,7 @@ def _roles(pieces, pair, ns, q_bufs, rng, epilogue="o_done", clean_first=False):
 
     def mma():
         at = n_q = 0
-        n_p = [0, 0]
+        n_p = [[0, 0], [0, 0]]
         commit = lambda *key: tensor.append(bar(*key))
 
         def qk(s, h):
@@ -94,14 +96,14 @@ def _roles(pieces, pair, ns, q_bufs, rng, epilogue="o_done", clean_first=False):
                     yield wait(("kv_full", at % ns), at // ns)
                     st_v, at = at % ns, at + 1
                     for s in range(2):
-                        yield wait(("p_full", s, 0), n_p[s])
+                        yield wait(("p_full", s, 0), n_p[s][0])
+                        n_p[s][0] += 1
                         pv(s, 0)
                         if more and s == 0:
                             yield wait(("kv_full", at % ns), at // ns)
                             st_k, at = at % ns, at + 1
                         if more:
                             qk(s, 0)
-                    n_p = [x + 1 for x in n_p]
                     if more:  # the last values' buffer is the softmax's, for its result
                         commit("kv_empty", st_v)
                         commit("kv_empty", st_k)
@@ -110,29 +112,45 @@ def _roles(pieces, pair, ns, q_bufs, rng, epilogue="o_done", clean_first=False):
                     if not more:
                         commit("o_done", 0)
                         commit("o_done", 1)
+            elif n == 1:  # one tile: a half for each stream
+                yield wait(("kv_full", at % ns), at // ns)
+                st_k, at = at % ns, at + 1
+                qk(0, 0)
+                qk(1, 1)
+                commit("kv_empty", st_k)
+                commit("q_empty", qb)
+                yield wait(("kv_full", at % ns), at // ns)
+                st_v, at = at % ns, at + 1
+                for s in range(2):
+                    yield wait(("p_full", s, s), n_p[s][s])
+                    n_p[s][s] += 1
+                    pv(s, s)
+                if few:
+                    commit("kv_empty", st_v)
+                commit("o_done", 0)
             else:
-                for i in range(min(n, 2)):
+                for i in range(2):
                     yield wait(("kv_full", at % ns), at // ns)
                     st_k, at = at % ns, at + 1
                     for h in range(steps):
                         qk(i, h)
                     commit("kv_empty", st_k)
-                if n <= 2:
+                if n == 2:
                     commit("q_empty", qb)
                 for i in range(n):
                     s, more = i & 1, i + 2 < n
                     yield wait(("kv_full", at % ns), at // ns)
                     st_v, at = at % ns, at + 1
                     for h in range(steps):
-                        yield wait(("p_full", s, h), n_p[s])
+                        yield wait(("p_full", s, h), n_p[s][h])
+                        n_p[s][h] += 1
                         pv(s, h)
                         if more and h == 0:
                             yield wait(("kv_full", at % ns), at // ns)
                             st_k, at = at % ns, at + 1
                         if more:
                             qk(s, h)
-                    n_p[s] += 1
-                    if i + 1 < n:
+                    if i + 1 < n or few:
                         commit("kv_empty", st_v)
                     if more:
                         commit("kv_empty", st_k)
@@ -152,7 +170,8 @@ def _roles(pieces, pair, ns, q_bufs, rng, epilogue="o_done", clean_first=False):
             yield ("poll", None, None)
 
     def softmax(s, warp):
-        n_t = n_o = n_piece = base = n_bar = 0
+        n_o = n_piece = base = n_bar = 0
+        n_s = [0, 0]
 
         def cta():
             nonlocal n_bar
@@ -161,32 +180,35 @@ def _roles(pieces, pair, ns, q_bufs, rng, epilogue="o_done", clean_first=False):
             return wait(("cta",), n_bar - 1)
 
         for n, masked in pieces:
-            for i in range(0 if pair else s, n, 1 if pair else 2):
+            halves = not pair and n == 1
+            for i in range(0 if pair or halves else s, n, 1 if pair else 2):
                 at = base + v_pos(i, n)
                 clean = masked and i >= n - 2 and (not pair or s == 0)
                 if clean and clean_first:  # planted: before the scores
                     yield wait(("kv_full", at % ns), at // ns)
                 for h in range(steps):
-                    yield wait(("s_full", s, h), n_t)
+                    if halves and h != s:
+                        continue
+                    yield wait(("s_full", s, h), n_s[h])
+                    n_s[h] += 1
                     if clean and h == 0:
                         yield wait(("kv_full", at % ns), at // ns)
-                    first = h == 0 and (i == 0 if pair else i < 2)
+                    first = halves or (h == 0 and (i == 0 if pair else i < 2))
                     if steps > 1 and not first and rng.random() < 0.3:  # the maximum moved
                         yield wait(("o_step", s), n_o - 1)
                     bar("p_full", s, h).arrive()
                     n_o += 1
-                n_t += 1
             base += 2 * n
             if epilogue == "o_done":
                 yield wait(("o_done", s if pair else 0), n_piece)
-            elif pair or s < n:  # planted: the last two steps by their own barrier
-                yield wait(("o_step", s), n_o - 2)
-                yield wait(("o_step", s), n_o - 1)
+            else:  # planted: the last two steps by their own barrier
+                for k in range(max(0, n_o - 2), n_o):
+                    yield wait(("o_step", s), k)
             n_piece += 1
             if not pair:
                 yield cta()
             yield cta()
-            if s == 0 and warp == 0:
+            if s == 0 and warp == 0 and not few:
                 bar("kv_empty", (base - 1) % ns).arrive()
 
     return [loads(True), loads(False), mma(), completions()] + [softmax(s, w) for s in range(2) for w in range(WARPS)]
