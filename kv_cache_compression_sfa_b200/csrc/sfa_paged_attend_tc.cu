@@ -10,8 +10,8 @@
 //   warps 4-7    the softmax of stream 1.
 // With more rows than one 128-row tile (PAIR) the streams are two row tiles that
 // share every key and value tile; with fewer they take the key tiles of one row
-// tile in turn, each with its own maximum, sum and output, which are joined in
-// tensor memory at the end.  Rows are (node, query head of the group), so that
+// tile in turn (or the halves of an only one), each with its own maximum, sum and
+// output, which are joined in tensor memory at the end.  Rows are (node, query head of the group), so that
 // one KV head's tile serves all of its query heads.
 //
 // Scores, P and their products go by steps: a whole tile with PAIR, where the
@@ -296,7 +296,7 @@ __device__ __forceinline__ void add_nonfinite(const AttendParams& p, const Atten
 // ways out of the first two cost a call of one token 0.6 us.
 // kFewSplit is kFew with P in two parts, for calls of up to kSplitResults values:
 // over so few the rounding of P does not average out, and the second product
-// is small beside the call (one token of 14 heads over 1,024: 11.1 against 10.8 us;
+// is small beside the call (one token of 14 heads over 1,024: 0.3 us of 10.5;
 // 256 sequences over some 2,500 would pay 216 against 187 us).
 enum TcMode { kFew = 0, kOne = 1, kPair = 2, kFewSplit = 3 };
 constexpr long long kSplitResults = 16384;
@@ -337,7 +337,8 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
   if (warp == kTcMmaWarp) tmem_alloc(&sh.tmem, kTmemCols);
   // Rows of q that no copy writes stay zero: their products cost the tensor
   // cores less power, which sets the clock of a card that streams a cache
-  // (256 sequences of one token for seconds: 237 us with whatever lay there).
+  // (256 sequences of one token for a second: 220 us, and 237 with whatever lay
+  // there; with products of 64 rows about 200).
   for (int i = tid; i < (PAIR ? 2 : 1) * P::tile / 16; i += kTcThreads)
     reinterpret_cast<uint4*>(smem + P::q)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
