@@ -256,6 +256,8 @@ def test_attend_tree(shape, dtype, ctx, lens, n, page):
     ("qwen7b", "bf16", [300, 0, 17], [200, 130, 1], 200, 64),      # several row tiles, causal
     ("qwen05b", "bf16", [1000], [150], 150, 16),
     ("tiny", "f32", [100, 3], [130, 129], 130, 32),
+    ("mqa", "bf16", [30, 0, 300, 9, 700], [500, 470, 1, 0, 333], 500, 64),   # many row tiles
+    ("tiny", "f32", [100, 0, 5], [600, 577, 3], 600, 32),
 ])
 def test_attend_chunk(shape, dtype, ctx, lens, n, page):
     Case(shape, dtype, ctx, lens, n, page, seed=13).check()
