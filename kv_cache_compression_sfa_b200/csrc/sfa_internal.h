@@ -286,8 +286,10 @@ constexpr int kAttendMaxBatch = 4096;  // sequences of an attend call (prefix su
 
 // An item's start and result weigh as much as this many tiles (32 trees of 16 over 17
 // .. 8,192 tokens: 45, 38, 40 and 46 us with 1, 2, 4 and 8; one tree of 64 over 65,500:
-// 92, 90, 83 and 80), unless the call has no more than kAttendSpread tiles a CTA.
+// 92, 90, 83 and 80), unless the call has no more than kAttendSpread tiles a CTA.  The
+// fp32 kernel's tiles take longer (8 trees of 16 over 1,024: 84 us with 2, 93 with 4).
 constexpr int kAttendItemCost = 4;
+constexpr int kAttendItemCostF32 = 2;
 constexpr int kAttendSpread = 2;
 
 // Rows of a work item and keys of a tile of the attend kernels, and the

@@ -316,7 +316,7 @@ AttendPlan attend_plan(int in_dtype, int head_dim, int G, int n_max, int n_sm) {
     attend_tc_rows(G, n_max, &a.rows_step, &a.kt);
   }
   a.n_cta = n_sm;
-  a.item_cost = kAttendItemCost;
+  a.item_cost = in_dtype == SFA_F32 ? kAttendItemCostF32 : kAttendItemCost;
   a.off_ml = static_cast<size_t>(align256(static_cast<long long>(sizeof(SplitMeta)) * a.n_cta));
   a.off_o = a.off_ml + static_cast<size_t>(align256(16LL * a.n_cta * a.rows_step));
   a.total = a.off_o + static_cast<size_t>(align256(8LL * a.n_cta * a.rows_step * head_dim));
