@@ -173,18 +173,21 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// P of N scores into tensor memory; returns its sum in 32 bits.  P is rounded to
-// bf16 for the tensor cores, into N / 2 columns: each weight is off by up to
-// 2^-8 of itself, which adds as much to a result as its own rounding does.  SPLIT
-// stores what the rounding left in another N / 2 columns (together 2^-16), for a
-// second product.
-template <int N, bool SPLIT>
+// P of N scores into tensor memory; returns its sum in 32 bits.  The tensor cores
+// take bf16.  One bf16 number would put each weight off by up to 2^-8 of itself and
+// add as much to a result as its own rounding does, so P is two: its rounding and
+// what that left (together within 2^-16 of it), in N / 2 columns each, for two
+// products.  Measured with two parts and with one: 256 sequences of 1,024 to 4,096
+// tokens 239 and 210 us, a tree of 64 over 65,500 tokens 111 and 88, chunks of
+// 2,048 tokens 243 and 187, one token over 1,024 11.0 and 10.9; errors against 64
+// bits (2-norm) 1.7e-3, which is the result's rounding, and 2.1 to 2.3e-3.
+template <int N>
 __device__ __forceinline__ float store_probs(float* x, float scale, float base, uint32_t taddr) {
   const float2 sc = make_float2(scale, scale), nb = make_float2(-base, -base);
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
   for (int c = 0; c < N; c += 64) {
-    uint32_t w[32], rest[SPLIT ? 32 : 1];
+    uint32_t w[32], rest[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
       const float2 e = fma2(make_float2(x[c + 2 * j], x[c + 2 * j + 1]), sc, nb);
@@ -192,15 +195,13 @@ __device__ __forceinline__ float store_probs(float* x, float scale, float base, 
       sum[j & 1] = add2(sum[j & 1], y);
       const __nv_bfloat162 b = __floats2bfloat162_rn(y.x, y.y);
       w[j] = *reinterpret_cast<const uint32_t*>(&b);
-      if (SPLIT) {
-        const float2 hi = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
-        const float2 lo = fma2(hi, make_float2(-1.f, -1.f), y);
-        const __nv_bfloat162 r = __floats2bfloat162_rn(lo.x, lo.y);
-        rest[j] = *reinterpret_cast<const uint32_t*>(&r);
-      }
+      const float2 hi = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+      const float2 lo = fma2(hi, make_float2(-1.f, -1.f), y);
+      const __nv_bfloat162 r = __floats2bfloat162_rn(lo.x, lo.y);
+      rest[j] = *reinterpret_cast<const uint32_t*>(&r);
     }
     tmem_st32(taddr + c / 2, w);
-    if (SPLIT) tmem_st32(taddr + N / 2 + c / 2, rest);
+    tmem_st32(taddr + N / 2 + c / 2, rest);
   }
   return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
@@ -294,17 +295,12 @@ __device__ __forceinline__ void add_nonfinite(const AttendParams& p, const Atten
 // Kernels by the rows of a call: up to 64 (products of 64 rows), one row tile, or
 // pairs of row tiles.  Each has its code alone: a switch at run time between the
 // ways out of the first two cost a call of one token 0.6 us.
-// kFewSplit is kFew with P in two parts, for calls of up to kSplitResults values:
-// over so few the rounding of P does not average out, and the second product
-// is small beside the call (one token of 14 heads over 1,024: 0.3 us of 10.5;
-// 256 sequences over some 2,500 would pay 216 against 187 us).
-enum TcMode { kFew = 0, kOne = 1, kPair = 2, kFewSplit = 3 };
-constexpr long long kSplitResults = 16384;
+enum TcMode { kFew = 0, kOne = 1, kPair = 2 };
 
 template <int D, int MODE>
 __global__ void __launch_bounds__(kTcThreads, 1)
 attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ TcMaps maps) {
-  constexpr bool PAIR = MODE == kPair, SPLIT = MODE == kFewSplit, m64 = MODE == kFew || SPLIT;
+  constexpr bool PAIR = MODE == kPair, m64 = MODE == kFew;
   using P = TcPlan<D, PAIR>;
   constexpr int NS = P::stages, HK = P::step, NH = P::steps;
   // the kernel has no other shared memory: the dynamic block starts on the 1024
@@ -500,11 +496,9 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
 #pragma unroll
           for (int k = 0; k < HK / 16; ++k)
             umma_bf16_ts(d, a + k * 8, b + ((k * 2048) >> 4), idesc_pv, k > 0 || !first);
-          if (SPLIT) {  // and what rounding P left
 #pragma unroll
-            for (int k = 0; k < HK / 16; ++k)
-              umma_bf16_ts(d, a + HK / 2 + k * 8, b + ((k * 2048) >> 4), idesc_pv, true);
-          }
+          for (int k = 0; k < HK / 16; ++k)  // and what rounding P left
+            umma_bf16_ts(d, a + HK / 2 + k * 8, b + ((k * 2048) >> 4), idesc_pv, true);
           if (NH > 1) umma_commit(&bars.o_step[s]);
         }
       };
@@ -687,7 +681,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
               }
             }
             // (rows that are not there get P = 0, as those of warps without rows have)
-            l += store_probs<HK, SPLIT>(x, p.scale_log2, r >= rows ? INFINITY : m == -INFINITY ? 0.f : m, t_s);
+            l += store_probs<HK>(x, p.scale_log2, r >= rows ? INFINITY : m == -INFINITY ? 0.f : m, t_s);
             tmem_st_wait();
           }
           tc_fence_before();
@@ -931,27 +925,20 @@ void attend_tc_rows(int G, int n_max, int* rows_step, int* kt) {
 
 cudaError_t attend_tc_prepare() {
   cudaError_t e = allow_tc<64, kFew>();
-  if (e == cudaSuccess) e = allow_tc<64, kFewSplit>();
   if (e == cudaSuccess) e = allow_tc<64, kOne>();
   if (e == cudaSuccess) e = allow_tc<64, kPair>();
   if (e == cudaSuccess) e = allow_tc<128, kFew>();
-  if (e == cudaSuccess) e = allow_tc<128, kFewSplit>();
   if (e == cudaSuccess) e = allow_tc<128, kOne>();
   if (e == cudaSuccess) e = allow_tc<128, kPair>();
   return e;
 }
 
 cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, cudaStream_t s) {
-  const long long results = static_cast<long long>(p.c.Lc) * p.c.B * p.c.n_max * p.c.nq * head_dim;
-  const int mode = p.c.n_max > kTcRows / p.c.G ? kPair
-                   : p.rows_step > kTcRows / 2 ? kOne
-                   : results <= kSplitResults  ? kFewSplit
-                                               : kFew;
+  const int mode = p.c.n_max > kTcRows / p.c.G ? kPair : p.rows_step > kTcRows / 2 ? kOne : kFew;
   const bool small = head_dim == 64;
   switch (mode) {
     case kPair: return small ? launch_tc<64, kPair>(p, s) : launch_tc<128, kPair>(p, s);
     case kOne: return small ? launch_tc<64, kOne>(p, s) : launch_tc<128, kOne>(p, s);
-    case kFewSplit: return small ? launch_tc<64, kFewSplit>(p, s) : launch_tc<128, kFewSplit>(p, s);
     default: return small ? launch_tc<64, kFew>(p, s) : launch_tc<128, kFew>(p, s);
   }
 }
