@@ -178,6 +178,14 @@ bool handle_ok(const sfa_handle* h) { return h != nullptr && h->magic == kHandle
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA; }
 
+// Makes the current device's context current to this host thread: the driver
+// refuses to encode tensor maps in a thread that has made no CUDA call yet (the
+// runtime's own calls see to it themselves).
+cudaError_t bind_context(int* device) {
+  const cudaError_t e = cudaGetDevice(device);
+  return e == cudaSuccess ? cudaSetDevice(*device) : e;
+}
+
 // Near-field plan of the prefill: on the tensor cores where they apply (bf16
 // inputs, k <= 16) unless h->near_mode is 0, there fused with the pool
 // scores unless it is 1; else on the CUDA cores.
@@ -235,7 +243,7 @@ constexpr long long kMaxSlots = 1LL << 30;  // of a sequence: slots and tile end
 // and SM count belong there.
 bool on_device(const sfa_handle* h) {
   int dev = -1;
-  return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
+  return bind_context(&dev) == cudaSuccess && dev == h->device;
 }
 
 int paged_status(const sfa_handle* h, int n_max, const int* ctx_lens, int batch) {
@@ -608,6 +616,8 @@ int prefill_impl(const sfa_handle* h, int layer_begin, int layer_count, const vo
   p.near = np;
   p.pool_smem = prefill_pool_smem();
   p.out_smem = prefill_out_smem();
+  int dev;
+  if (bind_context(&dev) != cudaSuccess) return SFA_ERR_CUDA;
   return cuda_status(launch_prefill(p, c->in_dtype, c->head_dim, s));
 }
 
@@ -660,6 +670,8 @@ int sfa_decode_step_ex(const sfa_handle* h, int layer_begin, int layer_count, co
   const bool tile = h->tile_ok && static_cast<long long>(layer_count) * n_seq <= 0x7fffffffLL &&
                     h->out_mode == SFA_OUT_F32 &&
                     (h->tile_mode == 1 || (h->tile_mode < 0 && n_seq >= kDecodeTileMinSeqs));
+  int dev;
+  if (tile && bind_context(&dev) != cudaSuccess) return SFA_ERR_CUDA;
   if (tile) return cuda_status(launch_decode_tile(p, c->in_dtype, c->head_dim, s));
   return cuda_status(launch_decode(p, c->in_dtype, c->head_dim, s));
 }
