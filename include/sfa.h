@@ -438,7 +438,9 @@ SFA_API int sfa_kv_append(const sfa_handle* h, const sfa_kv_cache* cache, int la
  * split over CTAs); 0 on invalid input.  It depends on n_max up to some
  * rows only, never on the lengths; its content need not be initialised.  A
  * workspace serves one call at a time: calls that may overlap on the GPU
- * (other streams, graphs replayed side by side) each need their own. */
+ * (other streams, graphs replayed side by side) each need their own, and so do
+ * calls of several host threads on one stream, whose launches (two a call) may
+ * mix.  It must live as long as a graph that captured the call. */
 SFA_API size_t sfa_kv_attend_workspace_bytes(const sfa_handle* h, int n_max);
 
 /* Exact attention of the new tokens, whose keys and values are in the cache

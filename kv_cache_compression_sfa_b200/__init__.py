@@ -702,6 +702,14 @@ def _plan_address() -> int:
     return _plan_addr
 
 
+def _stream_object(stream, device) -> torch.cuda.Stream:
+    """The Stream of a call's `stream`: a Stream, or a handle as an integer."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    ptr = _stream_ptr(stream)
+    return torch.cuda.ExternalStream(ptr, device=device) if ptr else torch.cuda.default_stream(device)
+
+
 def _zeros_for(shape, dtype, device, stream):
     """A zeroed tensor that work on `stream` may use: the fill comes first and
     the tensor is marked as used there."""
@@ -724,10 +732,10 @@ class SfaPagedCache:
 
     ``append``, ``attend`` and ``accept`` are sfa_kv_append, sfa_kv_attend and
     sfa_kv_accept for layers layer_begin .. layer_begin + q.shape[0] - 1; q is
-    [layers, B, n, n_q, d], ctx_lens and lens [B] int32 on the device.  The
-    workspace of attend belongs to the cache, one per stream; graphs that are
-    replayed side by side, and streams given as raw pointers, need a
-    ``workspace`` of their own per graph or stream."""
+    [layers, B, n, n_q, d], ctx_lens and lens [B] int32 on the device.  attend
+    takes its workspace from torch's allocator for the length of the call, in a
+    torch.cuda.graph capture from the graph's pool; a ``workspace`` that is given
+    serves one call at a time (host threads and graphs that share one take turns)."""
 
     def __init__(self, handle: Handle, k_pages: torch.Tensor, v_pages: torch.Tensor,
                  page_table: torch.Tensor):
@@ -744,7 +752,6 @@ class SfaPagedCache:
         tp = _need(page_table, "page_table", torch.int32, page_table.shape, dev)
         self.k_pages, self.v_pages, self.page_table = k_pages, v_pages, page_table
         self.c = sfa_kv_cache(kp, vp, self.n_pages, self.page_size, self.max_pages, tp)
-        self._ws, self._ws_need = {}, {}
         # what the calls, made once per layer and step, look up
         self._ref = ctypes.byref(self.c)
         self._index, self._dtype, self._lens_shape = dev, c.torch_dtype, (self.batch,)
@@ -754,31 +761,21 @@ class SfaPagedCache:
         self._spec = None
         if _fast is not None and dev >= 0:
             self._spec = _fast.spec(_address(lib.sfa_kv_append), _address(lib.sfa_kv_attend), _address(lib.sfa_kv_accept),
-                                    ctypes.addressof(self.c), dev, c.in_dtype == SFA_BF16, self.batch, *self._q_tail[:1],
+                                    _address(lib.sfa_kv_attend_workspace_bytes), ctypes.addressof(self.c), dev, c.in_dtype == SFA_BF16, self.batch, *self._q_tail[:1],
                                     *self._kv_tail)
 
     def _len_ptr(self, t, name: str) -> Optional[int]:
         return None if t is None else _need(t, name, torch.int32, self._lens_shape, self._index)
 
     def _workspace(self, n: int, stream) -> torch.Tensor:
-        """This stream's workspace, grown to what n new tokens need."""
-        need = self._ws_need.get(n)
-        if need is None:
-            need = self._ws_need[n] = sfa_kv_attend_workspace_bytes(self.handle, n)
-        if stream is None and 0 <= self._index != torch.cuda.current_device():
-            with torch.cuda.device(self._index):
-                key = _stream_ptr(None)
-        else:
-            key = _stream_ptr(stream)
-        ws = self._ws.get(key)
-        if ws is None or ws.numel() < need:
-            if ws is not None and isinstance(stream, torch.cuda.Stream):
-                ws.record_stream(stream)
-            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-            if isinstance(stream, torch.cuda.Stream):
-                ws.record_stream(stream)
-            self._ws[key] = ws
-        return ws
+        """A workspace for one call of n new tokens, from the pool of the call's
+        stream: it is free again for work behind the call, and in a capture it is
+        memory of the graph."""
+        need = sfa_kv_attend_workspace_bytes(self.handle, n)
+        if stream is None:
+            return torch.empty(need, dtype=torch.uint8, device=self.device)
+        with torch.cuda.stream(_stream_object(stream, self.device)):
+            return torch.empty(need, dtype=torch.uint8, device=self.device)
 
     def append(self, layer_begin: int, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
                ctx_lens: torch.Tensor, lens: Optional[torch.Tensor] = None,
@@ -836,8 +833,7 @@ class SfaPagedCache:
         sfa_tree_plan, or None: every new token sees those before it.  Rows past
         lens keep what out held (a new out is zero there)."""
         if self._spec is not None and out is not None and q.dim() == 5 and q.shape[2] > 0:
-            rc = _fast.attend(self._spec, self.handle.ptr, layer_begin, q, ctx_lens, lens, mask, out,
-                              self._workspace(q.shape[2], stream) if workspace is None else workspace,
+            rc = _fast.attend(self._spec, self.handle.ptr, layer_begin, q, ctx_lens, lens, mask, out, workspace,
                               None if stream is None else _stream_ptr(stream))
             if rc == SFA_OK:
                 return out

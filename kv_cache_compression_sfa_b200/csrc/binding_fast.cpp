@@ -9,6 +9,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -25,12 +26,14 @@ using PlanFn = decltype(&sfa_tree_plan);
 using AppendFn = decltype(&sfa_kv_append);
 using AttendFn = decltype(&sfa_kv_attend);
 using AcceptFn = decltype(&sfa_kv_accept);
+using BytesFn = decltype(&sfa_kv_attend_workspace_bytes);
 
 // What the calls of one cache share.
 struct Spec {
   AppendFn append;
   AttendFn attend;
   AcceptFn accept;
+  BytesFn attend_bytes;
   const sfa_kv_cache* cache;  // owned by the Python object that keeps this spec
   int device;
   at::ScalarType dtype;
@@ -95,21 +98,22 @@ PyObject* none() {
   Py_END_ALLOW_THREADS          \
   return PyLong_FromLong(rc);
 
-// spec(append, attend, accept, cache, device, is_bf16, batch, nq, nkv, d)
+// spec(append, attend, accept, attend_bytes, cache, device, is_bf16, batch, nq, nkv, d)
 PyObject* make_spec(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 10) return none();
+  if (n != 11) return none();
   Spec* s = new (std::nothrow) Spec;
   if (!s) return PyErr_NoMemory();
   s->append = reinterpret_cast<AppendFn>(PyLong_AsVoidPtr(a[0]));
   s->attend = reinterpret_cast<AttendFn>(PyLong_AsVoidPtr(a[1]));
   s->accept = reinterpret_cast<AcceptFn>(PyLong_AsVoidPtr(a[2]));
-  s->cache = static_cast<const sfa_kv_cache*>(PyLong_AsVoidPtr(a[3]));
-  s->device = static_cast<int>(PyLong_AsLong(a[4]));
-  s->dtype = PyObject_IsTrue(a[5]) ? at::kBFloat16 : at::kFloat;
-  s->batch = PyLong_AsLongLong(a[6]);
-  s->nq = PyLong_AsLongLong(a[7]);
-  s->nkv = PyLong_AsLongLong(a[8]);
-  s->d = PyLong_AsLongLong(a[9]);
+  s->attend_bytes = reinterpret_cast<BytesFn>(PyLong_AsVoidPtr(a[3]));
+  s->cache = static_cast<const sfa_kv_cache*>(PyLong_AsVoidPtr(a[4]));
+  s->device = static_cast<int>(PyLong_AsLong(a[5]));
+  s->dtype = PyObject_IsTrue(a[6]) ? at::kBFloat16 : at::kFloat;
+  s->batch = PyLong_AsLongLong(a[7]);
+  s->nq = PyLong_AsLongLong(a[8]);
+  s->nkv = PyLong_AsLongLong(a[9]);
+  s->d = PyLong_AsLongLong(a[10]);
   if (PyErr_Occurred()) {
     delete s;
     return nullptr;
@@ -162,26 +166,45 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                  static_cast<int>(B), qo, ko, st))
 }
 
-// attend(spec, handle, layer_begin, q, ctx, lens, mask, out, workspace, stream)
+// A workspace for the length of one call, from the pool of the call's stream: what
+// is enqueued there later may have the memory again, and a capture there takes it
+// from the graph's pool.
+struct Scratch {
+  void* p = nullptr;
+  ~Scratch() {
+    if (p) c10::cuda::CUDACachingAllocator::raw_delete(p);
+  }
+};
+
+// attend(spec, handle, layer_begin, q, ctx, lens, mask, out, workspace or None, stream)
 PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  const at::Tensor *q, *w;
-  if (n != 10 || !dims(a[3], 5, &q) || !dims(a[8], 1, &w)) return none();
+  const at::Tensor *q, *w = nullptr;
+  if (n != 10 || !dims(a[3], 5, &q) || (a[8] != Py_None && !dims(a[8], 1, &w))) return none();
   const Spec* s = spec_of(a[0]);
   if (!s) return none();
   const int64_t L = q->size(0), B = s->batch, m = q->size(2);
   if (L > INT32_MAX || m > INT32_MAX) return none();
-  void *qp, *cp, *lp, *mp, *op, *wp, *st;
+  void *qp, *cp, *lp, *mp, *op, *wp = nullptr, *st;
   const auto dt = s->dtype;
   const int dev = s->device;
   if (!take(a[3], dt, dev, {L, B, m, s->nq, s->d}, false, &qp) || !take(a[4], at::kInt, dev, {B}, false, &cp) ||
       !take(a[5], at::kInt, dev, {B}, true, &lp) || !take(a[6], at::kInt, dev, {B, m, (m + 31) / 32}, true, &mp) ||
       !take(a[7], dt, dev, {L, B, m, s->nq * s->d}, false, &op) ||
-      !take(a[8], at::kByte, dev, {w->size(0)}, false, &wp) || !stream_of(a[9], dev, &st))
+      (w && !take(a[8], at::kByte, dev, {w->size(0)}, false, &wp)) || !stream_of(a[9], dev, &st))
     return none();
   const sfa_handle* h = handle_of(a[1]);
   const long l0 = PyLong_AsLong(a[2]);
   if (PyErr_Occurred() || l0 < INT32_MIN || l0 > INT32_MAX) return none();
-  const size_t bytes = static_cast<size_t>(w->size(0));
+  Scratch own;
+  size_t bytes = w ? static_cast<size_t>(w->size(0)) : s->attend_bytes(h, static_cast<int>(m));
+  if (!w && bytes > 0) {
+    try {
+      own.p = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(bytes, static_cast<cudaStream_t>(st));
+    } catch (const std::exception&) {
+      return none();  // the caller's own way raises torch's error
+    }
+    wp = own.p;
+  }
   CALL(s->attend(h, s->cache, static_cast<int>(l0), static_cast<int>(L), qp, static_cast<int>(m),
                  static_cast<const int*>(lp), static_cast<const int*>(cp), static_cast<const uint32_t*>(mp),
                  static_cast<int>(B), op, wp, bytes, st))
