@@ -714,7 +714,8 @@ def _zeros_for(shape, dtype, device, stream):
     """A zeroed tensor that work on `stream` may use: the fill comes first and
     the tensor is marked as used there."""
     t = torch.zeros(shape, dtype=dtype, device=device)
-    if isinstance(stream, torch.cuda.Stream):
+    if stream is not None:
+        stream = _stream_object(stream, device)
         stream.wait_stream(torch.cuda.current_stream(device))
         t.record_stream(stream)
     return t

@@ -140,3 +140,33 @@ def test_a_given_workspace_is_used(path):
     assert torch.equal(out, want) and not bool((ws == 0x5A).all())
     with pytest.raises(sfa.SfaError):
         c.cache.attend(0, c.q, c.ctx_d, out=out, workspace=ws[:-1])
+
+
+@pytest.mark.parametrize("kind", ["stream", "pointer", "default pointer"])
+def test_new_outputs_on_another_stream(path, kind):
+    """The current stream is busy when it is to fill the new outputs: the fill must
+    not come after the call's results."""
+    c = _case(ctx=(300, 20))
+    parents = ints([[-1, 0], [-1, -1]])
+    rope = sfa.SfaRope()
+    k0, v0 = c.k_pages.clone(), c.v_pages.clone()
+
+    def step(stream=None):
+        pos, mask = sfa.sfa_tree_plan(c.h, parents, c.ctx_d, stream=stream)
+        qr, _ = c.cache.append(0, c.q, c.k, c.v, c.ctx_d, positions=pos, rope=rope, stream=stream)
+        return pos, mask, qr, c.cache.attend(0, qr, c.ctx_d, mask=mask, stream=stream)
+
+    want = step()
+    torch.cuda.synchronize()
+    s, busy = torch.cuda.Stream(), torch.cuda.Stream()
+    on = {"stream": s, "pointer": s.cuda_stream, "default pointer": 0}[kind]
+    for _ in range(3):
+        c.k_pages.copy_(k0)
+        c.v_pages.copy_(v0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(busy):
+            torch.cuda._sleep(3_000_000)
+            got = step(on)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert sfa.sfa_check_device_status(c.h) == sfa.SFA_OK

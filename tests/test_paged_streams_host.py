@@ -133,3 +133,26 @@ def test_a_workspace_comes_from_the_pool_of_the_calls_stream(cache, log, kind):
     _attend(cache, stream=s)
     (ptr,) = _workspaces(log)
     assert ("empty", ptr, 0 if kind == "default" else 0x200) in log
+
+
+@pytest.mark.parametrize("kind", ["stream", "pointer", "default"])
+@pytest.mark.parametrize("call", ["plan", "append", "attend"])
+def test_new_outputs_are_filled_before_the_call(cache, log, kind, call):
+    s = {"stream": FakeStream(0x200), "pointer": 0x200, "default": 0}[kind]
+    on = 0 if kind == "default" else 0x200
+    ctx = torch.zeros(3, dtype=torch.int32)
+    if call == "plan":
+        outs = sfa.sfa_tree_plan(cache.handle, torch.zeros(3, 4, dtype=torch.int32), ctx, stream=s)
+    elif call == "append":
+        k = torch.zeros(1, 3, 4, 2, 64, dtype=torch.bfloat16)
+        outs = cache.append(0, _q(4), k, k.clone(), ctx, stream=s)[:1]
+    else:
+        outs = [cache.attend(0, _q(4), ctx, workspace=torch.zeros(1 << 16, dtype=torch.uint8), stream=s)]
+    names = [e[0] for e in log]
+    at_call = max(i for i, n in enumerate(names) if n.startswith("sfa_"))
+    assert log[at_call][1][-1] == on
+    for t in outs:
+        fill = next(i for i, e in enumerate(log) if e[0] == "zeros" and e[1] == t.data_ptr())
+        if log[fill][2] != on:
+            assert ("wait", on, CURRENT) in log[fill:at_call], "the call's stream does not wait for the fill"
+            assert ("used on", t.data_ptr(), on) in log
