@@ -230,6 +230,43 @@ def _stream_ptr(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _stream_object(stream, device) -> torch.cuda.Stream:
+    """The Stream of a call's `stream`: a Stream, or a handle as an integer."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    ptr = _stream_ptr(stream)
+    return torch.cuda.ExternalStream(ptr, device=device) if ptr else torch.cuda.default_stream(device)
+
+
+def _hand_over(t: torch.Tensor, stream) -> None:
+    """Makes a tensor that is new on its device's current stream fit for use on
+    `stream`: the call comes after the memory's earlier use (and a fill), and the
+    allocator gives it to others only after the call."""
+    if stream is not None:
+        stream = _stream_object(stream, t.device)
+        stream.wait_stream(torch.cuda.current_stream(t.device))
+        t.record_stream(stream)
+
+
+def _empty_on(stream, nbytes: int, device) -> torch.Tensor:
+    """Uninitialised bytes from the pool of the call's stream: free again for
+    work behind the call, and in a torch.cuda.graph capture memory of the graph."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(_stream_object(stream, device)):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _capturing(stream, device) -> bool:
+    """Whether a graph is being captured on the call's stream."""
+    if device.type != "cuda":
+        return False
+    if stream is None and device.index in (None, torch.cuda.current_device()):
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(device), torch.cuda.stream(None if stream is None else _stream_object(stream, device)):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _is_cuda_tensor(t) -> bool:
     return isinstance(t, torch.Tensor) and t.is_cuda
 
@@ -489,20 +526,24 @@ class SfaOperator:
                            rows * cfg.hidden)
         self._in_dtype = cfg.torch_dtype
         self._decode_fn = load_library().sfa_decode_step
-        self.workspace = None
+        self.workspace, self._in_graph, self._kept = None, False, []
         if max_prefill > 0:
             self._ensure_workspace(max_prefill)
         self.reset()
 
     def _grow_workspace(self, need: int, stream=None):
-        """A workspace of at least `need` bytes.  The buffer it replaces may
-        still be in use by work enqueued on `stream`: it is marked as used
-        there, so the caching allocator hands it out again only after that
-        work."""
+        """A workspace of at least `need` bytes; one serves all calls, which the
+        operator's state puts in order.  The buffer that a larger one replaces may
+        still be in use by work enqueued on `stream`, and goes back behind it; one
+        that a graph has captured is kept as long as the operator."""
         if self.workspace is None or self.workspace.numel() < need:
-            if self.workspace is not None and isinstance(stream, torch.cuda.Stream):
-                self.workspace.record_stream(stream)
-            self.workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            if self.workspace is not None:
+                if self._in_graph:
+                    self._kept.append(self.workspace)
+                elif stream is not None:
+                    self.workspace.record_stream(_stream_object(stream, self.device))
+            self.workspace, self._in_graph = _empty_on(stream, need, self.device), False
+        self._in_graph = self._in_graph or _capturing(stream, self.device)
 
     def _ensure_workspace(self, n: int, stream=None):
         self._grow_workspace(sfa_prefill_workspace_bytes(self.handle, self.batch, n), stream)
@@ -513,14 +554,15 @@ class SfaOperator:
     def set_output_mode(self, mode: int) -> None:
         sfa_set_output_mode(self.handle, mode)
 
-    def _new_out(self, shape, stream=None):
-        """A result buffer allocated on the current stream; if the call runs
-        on another stream it is marked as used there too."""
+    def _new_out(self, shape, stream=None, fill: Optional[float] = None):
+        """A result buffer allocated (and filled) on the current stream and
+        handed over to the call's."""
         if self.handle.out_mode in (SFA_OUT_ADD_F32, SFA_OUT_ADD_BF16):
             raise ValueError("the add output modes need out: it holds the attention output")
         out = torch.empty(shape, dtype=self.handle.out_dtype, device=self.device)
-        if isinstance(stream, torch.cuda.Stream):
-            out.record_stream(stream)
+        if fill is not None:
+            out.fill_(fill)
+        _hand_over(out, stream)
         return out
 
     def prefill(self, q, k, v, out: Optional[torch.Tensor] = None, stream=None):
@@ -542,9 +584,7 @@ class SfaOperator:
         n = q.shape[2]
         c = self.cfg
         if out is None:
-            out = self._new_out((c.n_layers, self.batch, n, c.hidden), stream).fill_(float("nan"))
-            if isinstance(stream, torch.cuda.Stream):
-                stream.wait_stream(torch.cuda.current_stream())  # the fill comes first
+            out = self._new_out((c.n_layers, self.batch, n, c.hidden), stream, fill=float("nan"))
         if n > 0:
             self._ensure_workspace(n, stream)
             sfa_prefill_ragged(self.handle, q, k, v, n, lens, self.batch, self.state, out,
@@ -702,22 +742,9 @@ def _plan_address() -> int:
     return _plan_addr
 
 
-def _stream_object(stream, device) -> torch.cuda.Stream:
-    """The Stream of a call's `stream`: a Stream, or a handle as an integer."""
-    if isinstance(stream, torch.cuda.Stream):
-        return stream
-    ptr = _stream_ptr(stream)
-    return torch.cuda.ExternalStream(ptr, device=device) if ptr else torch.cuda.default_stream(device)
-
-
 def _zeros_for(shape, dtype, device, stream):
-    """A zeroed tensor that work on `stream` may use: the fill comes first and
-    the tensor is marked as used there."""
     t = torch.zeros(shape, dtype=dtype, device=device)
-    if stream is not None:
-        stream = _stream_object(stream, device)
-        stream.wait_stream(torch.cuda.current_stream(device))
-        t.record_stream(stream)
+    _hand_over(t, stream)
     return t
 
 
@@ -767,16 +794,6 @@ class SfaPagedCache:
 
     def _len_ptr(self, t, name: str) -> Optional[int]:
         return None if t is None else _need(t, name, torch.int32, self._lens_shape, self._index)
-
-    def _workspace(self, n: int, stream) -> torch.Tensor:
-        """A workspace for one call of n new tokens, from the pool of the call's
-        stream: it is free again for work behind the call, and in a capture it is
-        memory of the graph."""
-        need = sfa_kv_attend_workspace_bytes(self.handle, n)
-        if stream is None:
-            return torch.empty(need, dtype=torch.uint8, device=self.device)
-        with torch.cuda.stream(_stream_object(stream, self.device)):
-            return torch.empty(need, dtype=torch.uint8, device=self.device)
 
     def append(self, layer_begin: int, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
                ctx_lens: torch.Tensor, lens: Optional[torch.Tensor] = None,
@@ -855,7 +872,7 @@ class SfaPagedCache:
         if n == 0:
             return out
         if workspace is None:
-            workspace = self._workspace(n, stream)
+            workspace = _empty_on(stream, sfa_kv_attend_workspace_bytes(self.handle, n), self.device)
         size = workspace.numel()
         rc = _call_on(dev, stream, self._attend_fn, self.handle.ptr, self._ref, layer_begin, Lc, qp, n,
                       self._len_ptr(lens, "lens"), cp, mp, B, op,
