@@ -641,10 +641,19 @@ class SfaOperator:
 # ------------------------------------------------------ paged key/value cache
 
 
-try:  # the per-step calls without ctypes; the Python checks below serve where it is not built
-    from . import _fast
-except ImportError:
-    _fast = None
+def _load_fast():
+    """The per-step calls without ctypes, or None where they are not built, or
+    for another torch (whose tensors they would misread): the Python checks
+    below serve then."""
+    try:
+        from . import _fast
+        from .build import fast_stamp
+        return _fast if _fast.built_for == fast_stamp() else None
+    except (ImportError, AttributeError):
+        return None
+
+
+_fast = _load_fast()
 
 
 def _address(fn) -> int:

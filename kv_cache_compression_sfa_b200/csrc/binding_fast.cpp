@@ -248,4 +248,11 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, kMethods, nu
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__fast() { return PyModule_Create(&kModule); }
+PyMODINIT_FUNC PyInit__fast() {
+  PyObject* m = PyModule_Create(&kModule);
+  if (m && PyModule_AddStringConstant(m, "built_for", SFA_BUILT_FOR) < 0) {  // torch and Python, by the build
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
