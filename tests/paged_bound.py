@@ -3,8 +3,9 @@ bound of a kernel that loses nothing but the result's rounding.
 
 As in paged_reference (S = sum_j p_j |v_j|, A the largest sum_i |q_i k_ji| /
 sqrt(d), N visible keys, u = 2^-24, h half a step of the result's type), but for
-P: its two bf16 parts leave at most 2^-8 * 2^-8 of a weight, which enters numerator
-and denominator, so 2 * 2^-16 takes the place of 2 * 2^-8.
+P: its upper half word leaves a rest below 2^-7 of a weight, whose bf16 is off by
+2^-8 of itself at most, and the rest carries 2^-22 of the weight more.  That enters
+numerator and denominator, so 2 * (2^-15 + 2^-22) takes the place of 2 * 2^-8.
 """
 import math
 
@@ -22,7 +23,7 @@ def attend(q, k_pages, v_pages, table, ctx, lens, mask_rows=None, layer_begin=0)
     G = nq // nkv
     out = torch.full((Lc, B, n, nq * d), math.nan, dtype=torch.float64)
     bound = torch.zeros_like(out)
-    p_round = 2 * 2.0 ** -16 if q.dtype == torch.bfloat16 else 0.0
+    p_round = 2 * (2.0 ** -15 + 2.0 ** -22) if q.dtype == torch.bfloat16 else 0.0
     for l in range(Lc):
         for b in range(B):
             if lens[b] == 0:
