@@ -329,11 +329,13 @@ SFA_API int sfa_prefill_ragged(const sfa_handle* h, const void* q, const void* k
 SFA_API int sfa_prefill_static_ws(const sfa_handle* h, const void* q, const void* k, const void* v,
                                   long long n, int batch, void* state, void* out, void* stream);
 
-/* Test hook for the device-side bounded waits of sfa_prefill (not needed in
- * normal use).  withhold_tile: tile index (tile * streams + stream, streams =
+/* Test hook for the device-side bounded waits of sfa_prefill and of the bf16
+ * sfa_kv_attend (not needed in normal use).  sfa_prefill: withhold_tile: tile index (tile * streams + stream, streams =
  * layers x batch of the call) whose pool-weight CTA waits on a barrier that
  * nothing completes (-1 disables); spin_limit: polls before that wait gives
- * up and latches SFA_ERR_DEVICE_TIMEOUT (0 restores the default).  The
+ * up and latches SFA_ERR_DEVICE_TIMEOUT (0 restores the default).  sfa_kv_attend:
+ * withhold_tile 0, 4, 8, 9 or 10 is the warp (first of four for 0 and 4) that begins
+ * with such a wait, and spin_limit bounds every wait of the call.  The
  * kernel still finishes and the context stays usable.  Affects later calls
  * on this handle only. */
 SFA_API int sfa_debug_set_wait_limit(sfa_handle* h, unsigned int spin_limit, long long withhold_tile);

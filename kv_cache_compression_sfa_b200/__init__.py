@@ -483,9 +483,11 @@ def sfa_check_device_status(h: Handle, stream=None) -> int:
 
 
 def sfa_debug_set_wait_limit(h: Handle, spin_limit: int = 0, withhold_tile: int = -1) -> None:
-    """Test hook of the prefill's bounded waits: the pool CTA of tile
+    """Test hook of the bounded waits.  Prefill: the pool CTA of tile
     `withhold_tile` (tile * streams + stream) waits on a barrier that nothing
-    completes, giving up after `spin_limit` polls (0: default); -1 disables."""
+    completes, giving up after `spin_limit` polls (0: default); -1 disables.
+    Paged attention in bf16: a role of every CTA begins with such a wait (0, 4
+    softmax, 8 keys, 9 products, 10 values), and its others give up as early."""
     rc = load_library().sfa_debug_set_wait_limit(h.ptr, spin_limit, withhold_tile)
     if rc != SFA_OK:
         raise SfaError(rc, "sfa_debug_set_wait_limit")

@@ -846,6 +846,9 @@ int sfa_kv_attend(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begi
   p.item_cost = a.item_cost;
   p.spread = kAttendSpread;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(c->head_dim)));
+  const bool hook = h->withhold_tile >= 0;
+  p.wait_limit = hook ? h->spin_limit : kAttendPollLimit;
+  p.withhold = hook ? static_cast<int>(std::min<long long>(h->withhold_tile, 1 << 20)) : -1;
   p.meta = reinterpret_cast<SplitMeta*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + a.off_ml);
   p.part_o = reinterpret_cast<float*>(ws + a.off_o);

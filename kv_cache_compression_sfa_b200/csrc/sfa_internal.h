@@ -277,11 +277,14 @@ struct AttendParams {
   int n_cta;                // CTAs that share the tiles
   int item_cost, spread;    // tiles that an item's start and result weigh, from `spread` tiles a CTA on
   float scale_log2;         // log2(e) / sqrt(d)
+  unsigned wait_limit;      // polls of a bounded wait before it gives up (bf16)
+  int withhold;             // test hook: the warp (of a softmax stream the first) whose role begins with a wait for nothing; -1
   SplitMeta* meta;          // [n_cta]
   float* part_ml;           // [n_cta][2][rows_step][2]: running maximum (log2 units), sum
   float* part_o;            // [n_cta][2][rows_step][D], unnormalised
 };
 
+constexpr unsigned kAttendPollLimit = 1u << 20;
 constexpr int kAttendMaxBatch = 4096;  // sequences of an attend call (prefix sums in shared memory)
 
 // An item's start and result weigh as much as this many tiles (32 trees of 16 over 17

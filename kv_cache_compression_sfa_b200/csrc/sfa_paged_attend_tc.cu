@@ -47,7 +47,7 @@ constexpr int kTcValueWarp = 10;
 constexpr int kTcKeys = 128;     // keys of a tile
 constexpr int kTcRows = 128;     // rows of a row tile (tensor-memory lanes)
 constexpr uint32_t kTmemCols = 512;
-constexpr unsigned kTcPollLimit = 1u << 20;  // polls of a bounded wait
+constexpr unsigned kTcPollLimit = kAttendPollLimit;
 constexpr float kRescaleLog2 = 8.0f;  // the maximum moves only when it grows by more than this (log2)
 
 // Shared memory: q (one row tile, or two), then the ring; all blocks
@@ -81,6 +81,7 @@ struct TcShared {
   TcBars bars;
   float2 ml[2][kTcRows];  // maximum and sum of both streams' rows
   int bad[2][2];          // [piece & 1][stream]: clean_values found elements that are not finite
+  unsigned kv_fills[12], q_fills[2];  // copies issued into every buffer, for an exit after a wait that ran out
   uint32_t tmem;
 };
 
@@ -329,6 +330,8 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       mbar_init(&bars.o_done[s], 1);
       sh.bad[0][s] = sh.bad[1][s] = 0;
     }
+    for (int i = 0; i < NS; ++i) sh.kv_fills[i] = 0u;
+    sh.q_fills[0] = sh.q_fills[1] = 0u;
     mbar_init(&bars.drain, 1);
     mbar_fence_init();
   }
@@ -354,6 +357,11 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
   const int q_next = m64 ? (p.rows_step + 7) / 8 * 1024 : 0;
   const int tile_rows = PAIR ? p.rows_step / 2 : p.rows_step;  // rows of one row tile
   bool ok = true;
+  // Every wait has a limit.  A role whose wait runs out stops, and those that wait
+  // for it run out in turn; the exit below ends what is then in flight.
+  const unsigned limit = p.wait_limit;
+  if (p.withhold >= 0 && p.withhold == (warp >= kTcKeyWarp ? warp : warp >> 2 << 2))  // a test's role
+    ok = mbar_wait_bounded(&bars.drain, 0, limit, p.c.err);
 
   if (warp >= kTcKeyWarp) {
   if constexpr (PAIR) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTcOtherRegs));
@@ -371,7 +379,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
     const int my_page = lane % ppt, my_half = lane / ppt;
     const unsigned box_off = static_cast<unsigned>(my_half * (kTcKeys * 128) + my_page * prow * 128);
     const int z_none = static_cast<int>(static_cast<long long>(p.c.nkv) * p.c.n_pages * (p.c.l0 + p.c.Lc));
-    unsigned base = 0, last = 0, filled = 0;  // ring position of the piece; of this warp's last buffers
+    unsigned base = 0;  // ring position of the piece
     int n_q = 0;
     for (PieceWalk w(run); w.more() && ok; w.next(p)) {
       const int n = w.t1 - w.t0;
@@ -386,7 +394,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
         const unsigned at = base + static_cast<unsigned>(PAIR ? 2 * i + (keys ? 0 : 1) : keys ? (i < 2 ? i : 2 * i - 1)
                                                                                         : (n == 1 ? 1 : min(2 * i + 2, n + i)));
         const unsigned st = at % NS, turn = at / NS;
-        if (turn > 0) ok = ok && mbar_wait_bounded(&bars.kv_empty[st], (turn - 1) & 1u, kTcPollLimit, p.c.err);
+        if (turn > 0) ok = ok && mbar_wait_bounded(&bars.kv_empty[st], (turn - 1) & 1u, limit, p.c.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         const int t = w.t0 + i;
@@ -395,24 +403,26 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
           z = (z_head + pg) * p.c.nkv + w.it.kh;
         else if (lane < boxes && t * kTcKeys + my_page * prow < w.it.kv_end)
           latch_error(p.c.err, SFA_ERR_INVALID_ARG);  // a page that is needed: read as zeros
-        if (lane == 0) mbar_arrive_expect_tx(&bars.kv_full[st], P::tile);
+        if (lane == 0) {
+          sh.kv_fills[st] = turn + 1;
+          mbar_arrive_expect_tx(&bars.kv_full[st], P::tile);
+        }
         __syncwarp();
         if (lane < boxes)
           tma_load_3d(smem + P::ring + st * P::tile + box_off, map, my_half * 64, (t * kTcKeys) & (p.c.ps - 1) & ~(prow - 1), z,
                       &bars.kv_full[st]);
-        last = at;
-        ++filled;
       };
       // q goes behind the item's first keys: its buffer may still be in use
       auto load_q = [&]() {
         const int qb = n_q % q_bufs, turn = n_q / q_bufs;
         if (turn > 0)
-          ok = ok && mbar_wait_bounded(&bars.q_empty[qb], static_cast<unsigned>((turn - 1) & 1), kTcPollLimit, p.c.err);
+          ok = ok && mbar_wait_bounded(&bars.q_empty[qb], static_cast<unsigned>((turn - 1) & 1), limit, p.c.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         const int node0 = p.by_group(w.it.row0);
         const int nb = p.by_group(tile_rows);
         if (lane == 0) {
+          sh.q_fills[qb] = static_cast<unsigned>(turn + 1);
           mbar_arrive_expect_tx(&bars.q_full[qb], static_cast<unsigned>(tile_rows * 128 * (D / 64) * (PAIR ? 2 : 1)));
           for (int s = 0; s < (PAIR ? 2 : 1); ++s)
             for (int h = 0; h < D / 64; ++h)
@@ -436,12 +446,6 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       }
       base += 2u * static_cast<unsigned>(n);
     }
-    if (!ok) {  // no copy may land after the CTA has left: this warp's fills of the last NS positions
-      for (unsigned at = last < NS ? 0u : last - NS + 1; filled > 0 && at <= last; ++at)
-        mbar_wait_bounded(&bars.kv_full[at % NS], (at / NS) & 1u, kTcPollLimit, p.c.err);
-      for (int i = max(0, n_q - q_bufs); i < n_q; ++i)
-        mbar_wait_bounded(&bars.q_full[i % q_bufs], static_cast<unsigned>((i / q_bufs) & 1), kTcPollLimit, p.c.err);
-    }
   } else if (warp == kTcMmaWarp) {
     // ---- products.  The whole warp walks and waits, so that addresses stay
     // uniform; one elected lane issues.
@@ -457,7 +461,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       int n_q = 0;
       unsigned n_p[2][2] = {{0u, 0u}, {0u, 0u}};  // [stream][step]: how often its P was waited for
       auto wait = [&](uint64_t* bar, unsigned parity) {
-        ok = ok && mbar_wait_bounded(bar, parity & 1u, kTcPollLimit, p.c.err);
+        ok = ok && mbar_wait_bounded(bar, parity & 1u, limit, p.c.err);
         ok = __all_sync(0xffffffffu, ok);  // no lane may fall two phases behind
         tc_fence_after();
         return ok;
@@ -579,10 +583,6 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
         }
         if (!ok) break;
       }
-      if (!ok) {  // products in flight end before tensor memory is freed
-        if (leader) umma_commit(&bars.drain);
-        mbar_wait_bounded(&bars.drain, 0, kTcPollLimit, p.c.err);
-      }
     }
     __syncwarp();
   }
@@ -619,7 +619,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
           const bool first = halves || (h == 0 && (PAIR ? i == 0 : i < 2));
           RowMask<HK> vis;
           if (masked) vis = row_mask<HK>(p, it, node, t * kTcKeys + h * HK);
-          ok = mbar_wait_bounded(&bars.s_full[s][h], (h == 0 ? n_s[0] : n_s[1]) & 1u, kTcPollLimit, p.c.err);
+          ok = mbar_wait_bounded(&bars.s_full[s][h], (h == 0 ? n_s[0] : n_s[1]) & 1u, limit, p.c.err);
           h == 0 ? ++n_s[0] : ++n_s[1];
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -629,7 +629,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
             // buffer's phase can be told from its last but one.
             const unsigned at = n_kv + static_cast<unsigned>(PAIR ? 2 * i + 1 : (n == 1 ? 1 : min(2 * i + 2, n + i)));
             const unsigned st = at % NS;
-            ok = mbar_wait_bounded(&bars.kv_full[st], (at / NS) & 1u, kTcPollLimit, p.c.err);
+            ok = mbar_wait_bounded(&bars.kv_full[st], (at / NS) & 1u, limit, p.c.err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             clean_values<D>(smem + P::ring + st * P::tile, full_end - t * kTcKeys, it.kv_end - t * kTcKeys, tl,
@@ -668,7 +668,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
               // O holds the step before the last of this stream (these scores came
               // after it); with two steps a tile the last one is waited for
               if (NH > 1) {
-                ok = mbar_wait_bounded(&bars.o_step[s], (n_o - 1u) & 1u, kTcPollLimit, p.c.err);
+                ok = mbar_wait_bounded(&bars.o_step[s], (n_o - 1u) & 1u, limit, p.c.err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
               }
@@ -697,7 +697,7 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       n_kv += 2u * static_cast<unsigned>(n);
       // ---- result of the piece
       const bool starts = w.t0 == 0, whole = starts && w.t1 == it.nt;
-      ok = ok && mbar_wait_bounded(&bars.o_done[PAIR ? s : 0], n_piece & 1u, kTcPollLimit, p.c.err);
+      ok = ok && mbar_wait_bounded(&bars.o_done[PAIR ? s : 0], n_piece & 1u, limit, p.c.err);
       ok = __all_sync(0xffffffffu, ok);
       if (!PAIR) {
         sh.ml[s][tl] = make_float2(m, l);
@@ -833,16 +833,27 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
       named_bar_sync(1, kTcSoftmaxThreads);
       if (tid == 0) {
         sh.bad[n_piece & 1u][0] = sh.bad[n_piece & 1u][1] = 0;
-        if (!m64) mbar_arrive(&bars.kv_empty[st_last]);
+        if (!m64 && ok) mbar_arrive(&bars.kv_empty[st_last]);
       }
       ++n_piece;
     }
     if (!wrote && tid == 0) write_meta(p, run, false, run.it, 0);
   }
   tc_fence_before();
-  __syncthreads();
+  const bool all_ok = __syncthreads_and(ok);
   if (warp == kTcMmaWarp) {
     tc_fence_after();
+    // After a wait that ran out: products end before tensor memory is freed, and
+    // copies land before the CTA leaves its shared memory to another.
+    if (!all_ok) {
+      if (elect_one()) umma_commit(&bars.drain);
+      mbar_wait_bounded(&bars.drain, 0, kTcPollLimit, p.c.err);
+      for (int i = 0; i < NS; ++i)
+        if (sh.kv_fills[i] > 0) mbar_wait_bounded(&bars.kv_full[i], (sh.kv_fills[i] - 1) & 1u, kTcPollLimit, p.c.err);
+      for (int i = 0; i < q_bufs; ++i)
+        if (sh.q_fills[i] > 0) mbar_wait_bounded(&bars.q_full[i], (sh.q_fills[i] - 1) & 1u, kTcPollLimit, p.c.err);
+      __syncwarp();
+    }
     tmem_dealloc(tmem, kTmemCols);
   }
 }
