@@ -243,7 +243,7 @@ constexpr long long kMaxSlots = 1LL << 30;  // of a sequence: slots and tile end
 // and SM count belong there.
 bool on_device(const sfa_handle* h) {
   int dev = -1;
-  return bind_context(&dev) == cudaSuccess && dev == h->device;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
 }
 
 int paged_status(const sfa_handle* h, int n_max, const int* ctx_lens, int batch) {
@@ -831,6 +831,8 @@ int sfa_kv_attend(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begi
   if (tiles > 1073741824.0) return SFA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < a.total) return SFA_ERR_WORKSPACE;
   if (!on_device(h)) return SFA_ERR_INVALID_ARG;
+  int dev;
+  if (c->in_dtype == SFA_BF16 && bind_context(&dev) != cudaSuccess) return SFA_ERR_CUDA;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   p.q = q;
   p.out = out;

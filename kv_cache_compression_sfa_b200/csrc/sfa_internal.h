@@ -284,8 +284,8 @@ struct AttendParams {
   float* part_o;            // [n_cta][2][rows_step][D], unnormalised
 };
 
-constexpr unsigned kAttendPollLimit = 1u << 20;
-constexpr int kAttendMaxBatch = 4096;  // sequences of an attend call (prefix sums in shared memory)
+constexpr unsigned kAttendPollLimit = 1u << 20;  // polls of a bounded wait of the bf16 kernels
+constexpr int kAttendMaxBatch = 4096;  // sequences of an attend call (every warp looks over their lengths)
 
 // An item's start and result weigh as much as this many tiles (32 trees of 16 over 17
 // .. 8,192 tokens: 45, 38, 40 and 46 us with 1, 2, 4 and 8; one tree of 64 over 65,500:
