@@ -458,7 +458,7 @@ SFA_API size_t sfa_kv_attend_workspace_bytes(const sfa_handle* h, int n_max);
  * with n_max > SFA_TREE_MAX, batch > 4096, layer_count * batch * n_max * n_q >
  * 2^31 - 1, or more than 2^30 key tiles over all layers, sequences, KV heads and
  * row tiles at max_pages full pages (tiles of 128 keys, 64 in fp32; an item, which
- * is one row tile of a KV head, counts 4 more, 2 in fp32).
+ * is one row tile of a KV head, counts up to 4 more).
  * SFA_ERR_WORKSPACE if workspace is too small.  A device-side wait that runs out
  * is latched as SFA_ERR_DEVICE_TIMEOUT; that call's out is incomplete. */
 SFA_API int sfa_kv_attend(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begin, int layer_count,

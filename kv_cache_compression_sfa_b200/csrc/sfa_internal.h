@@ -287,12 +287,13 @@ struct AttendParams {
 constexpr unsigned kAttendPollLimit = 1u << 20;  // polls of a bounded wait of the bf16 kernels
 constexpr int kAttendMaxBatch = 4096;  // sequences of an attend call (every warp looks over their lengths)
 
-// An item's start and result weigh as much as this many tiles (32 trees of 16 over 17
-// .. 8,192 tokens: 45, 38, 40 and 46 us with 1, 2, 4 and 8; one tree of 64 over 65,500:
-// 92, 90, 83 and 80), unless the call has no more than kAttendSpread tiles a CTA.  The
-// fp32 kernel's tiles take longer (8 trees of 16 over 1,024: 84 us with 2, 93 with 4).
-constexpr int kAttendItemCost = 4;
-constexpr int kAttendItemCostF32 = 2;
+// An item's start and result weigh as much as this many tiles, unless the call has no
+// more than kAttendSpread tiles a CTA.  With 1, 2, 4 and 8: up to one row tile in bf16,
+// 32 trees of 16 over 17 .. 8,192 tokens 36, 33, 36 and 40 us and 256 tokens over 1,024
+// .. 4,096 201, 200, 207 and 221; pairs of row tiles, a tree of 64 over 65,500 tokens
+// 102, 100, 92 and 92; fp32, 8 trees of 16 over 1,024, 84 with 2 and 93 with 4.
+constexpr int kAttendItemCost = 2;
+constexpr int kAttendItemCostPairs = 4;
 constexpr int kAttendSpread = 2;
 
 // Rows of a work item and keys of a tile of the attend kernels, and the
@@ -308,7 +309,7 @@ cudaError_t launch_kv_append(const AppendParams& p, int in_dtype, int head_dim, 
 cudaError_t launch_kv_accept(const AcceptParams& p, int in_dtype, int head_dim, cudaStream_t s);
 cudaError_t launch_kv_attend(const AttendParams& p, int in_dtype, int head_dim, cudaStream_t s);
 cudaError_t attend_prepare(int device);
-void attend_tc_rows(int G, int n_max, int* rows_step, int* kt);
+void attend_tc_rows(int G, int n_max, AttendPlan* a);
 cudaError_t attend_tc_prepare();
 cudaError_t launch_attend_tc(const AttendParams& p, int head_dim, cudaStream_t s);
 

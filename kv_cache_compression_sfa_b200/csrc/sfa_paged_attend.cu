@@ -311,12 +311,12 @@ AttendPlan attend_plan(int in_dtype, int head_dim, int G, int n_max, int n_sm) {
   AttendPlan a;
   if (in_dtype == SFA_F32) {
     a.kt = kSimtKeys;
+    a.item_cost = kAttendItemCost;
     a.rows_step = kSimtWarps * simt_rpw(static_cast<int>(std::min<long long>(static_cast<long long>(n_max) * G, 64)));
   } else {
-    attend_tc_rows(G, n_max, &a.rows_step, &a.kt);
+    attend_tc_rows(G, n_max, &a);
   }
   a.n_cta = n_sm;
-  a.item_cost = in_dtype == SFA_F32 ? kAttendItemCostF32 : kAttendItemCost;
   a.off_ml = static_cast<size_t>(align256(static_cast<long long>(sizeof(SplitMeta)) * a.n_cta));
   a.off_o = a.off_ml + static_cast<size_t>(align256(16LL * a.n_cta * a.rows_step));
   a.total = a.off_o + static_cast<size_t>(align256(8LL * a.n_cta * a.rows_step * head_dim));

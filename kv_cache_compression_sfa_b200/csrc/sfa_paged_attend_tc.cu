@@ -655,11 +655,11 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
 #pragma unroll
             for (int j = 4; j + 1 < HK; j += 2) mx[(j >> 1) & 3] = max3(mx[(j >> 1) & 3], x[j], x[j + 1]);
             const float top = max3(mx[0], mx[1], max3(mx[2], mx[3], mx[3])) * p.scale_log2;
-            // the maximum in use may lag behind by 2^8, which fp32 sums and outputs hold easily
+            // the maximum in use may lag behind by 2^8 (and 1), which fp32 sums and outputs hold easily
             const bool move = !(top <= m + kRescaleLog2);  // a NaN score moves it to NaN, and the row with it
             float fix = 1.f;
-            if (move) {  // to a whole power of two: P's digits, and so its rounding, are the same under any m
-              const float to = ceilf(top);
+            if (move) {  // to a whole power of two: P's digits, and so its rounding, hardly depend on m
+              const float to = floorf(top);
               fix = exp2_approx(m - to);
               m = to;
               l *= fix;
@@ -931,10 +931,12 @@ cudaError_t allow_tc() {
 
 // Nodes of a row tile; the call takes two row tiles at a time when its nodes
 // do not fit one.
-void attend_tc_rows(int G, int n_max, int* rows_step, int* kt) {
+void attend_tc_rows(int G, int n_max, AttendPlan* a) {
   const int nodes = kTcRows / G;
-  *rows_step = n_max <= nodes ? n_max * G : 2 * nodes * G;
-  *kt = kTcKeys;
+  const bool pairs = n_max > nodes;
+  a->rows_step = pairs ? 2 * nodes * G : n_max * G;
+  a->kt = kTcKeys;
+  a->item_cost = pairs ? kAttendItemCostPairs : kAttendItemCost;
 }
 
 cudaError_t attend_tc_prepare() {
