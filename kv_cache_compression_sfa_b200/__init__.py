@@ -719,19 +719,19 @@ def sfa_tree_plan(h: Handle, parents: torch.Tensor, ctx_lens: torch.Tensor,
     if not isinstance(parents, torch.Tensor) or parents.dim() != 2:
         raise ValueError("parents must be a [batch, n] tensor")
     B, n = parents.shape
-    if _fast is not None and positions is not None and mask is not None and parents.is_cuda:
-        rc = _fast.plan(_plan_address(), h.ptr, parents, ctx_lens, lens, positions, mask,
-                        None if stream is None else _stream_ptr(stream))
-        if rc == SFA_OK:
-            return positions, mask
-        if rc is not None:
-            raise SfaError(rc, "sfa_tree_plan")
     dev, i32 = parents.get_device(), torch.int32
     words = (n + 31) // 32
     if positions is None:
         positions = _zeros_for((B, n), i32, parents.device, stream)
     if mask is None:
         mask = _zeros_for((B, n, words), i32, parents.device, stream)
+    if _fast is not None and parents.is_cuda:
+        rc = _fast.plan(_plan_address(), h.ptr, parents, ctx_lens, lens, positions, mask,
+                        None if stream is None else _stream_ptr(stream))
+        if rc == SFA_OK:
+            return positions, mask
+        if rc is not None:
+            raise SfaError(rc, "sfa_tree_plan")
     rc = _call_on(dev, stream, load_library().sfa_tree_plan, h.ptr,
                   _need(parents, "parents", i32, (B, n), dev), n,
                   None if lens is None else _need(lens, "lens", i32, (B,), dev),
@@ -814,7 +814,10 @@ class SfaPagedCache:
         """Rotated keys and values of the new tokens into their pages; returns
         (q_out, k_out), the rotated queries (a new tensor unless given; None
         without q) and keys (None unless given)."""
-        if self._spec is not None and (q is None or q_out is not None):
+        if q is not None and q_out is None:
+            _need(q, "q", self._dtype, q.shape, self._index)
+            q_out = _zeros_for(q.shape, self._dtype, self.device, stream)
+        if self._spec is not None:
             if rope is not None:
                 rope.check(self._kv_tail[1])
             rc = _fast.append(self._spec, self.handle.ptr, layer_begin, q, k, v, ctx_lens, lens, positions,
@@ -833,8 +836,6 @@ class SfaPagedCache:
         qp = qo = ko = None
         if q is not None:
             qp = _need(q, "q", dt, qs, dev)
-            if q_out is None:
-                q_out = _zeros_for(qs, dt, self.device, stream)
             qo = _need(q_out, "q_out", dt, qs, dev)
         elif q_out is not None:
             raise ValueError("q_out needs q")
@@ -861,7 +862,12 @@ class SfaPagedCache:
         out [layers, B, n, hidden] in the input dtype.  mask [B, n, words] as of
         sfa_tree_plan, or None: every new token sees those before it.  Rows past
         lens keep what out held (a new out is zero there)."""
-        if self._spec is not None and out is not None and q.dim() == 5 and q.shape[2] > 0:
+        if out is None:
+            if q.dim() != 5:
+                raise ValueError("q must be [layers, batch, n, n_q, d]")
+            _need(q, "q", self._dtype, q.shape, self._index)
+            out = _zeros_for(q.shape[:3] + (self._q_tail[0] * self._q_tail[1],), self._dtype, self.device, stream)
+        if self._spec is not None and q.dim() == 5 and q.shape[2] > 0:
             rc = _fast.attend(self._spec, self.handle.ptr, layer_begin, q, ctx_lens, lens, mask, out, workspace,
                               None if stream is None else _stream_ptr(stream))
             if rc == SFA_OK:
@@ -877,8 +883,6 @@ class SfaPagedCache:
         cp = _need(ctx_lens, "ctx_lens", torch.int32, self._lens_shape, dev)
         mp = None if mask is None else _need(mask, "mask", torch.int32, (B, n, (n + 31) // 32), dev)
         hidden = self._q_tail[0] * self._q_tail[1]
-        if out is None:
-            out = _zeros_for(rows + (hidden,), dt, self.device, stream)
         op = _need(out, "out", dt, rows + (hidden,), dev)
         if n == 0:
             return out

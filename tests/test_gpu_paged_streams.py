@@ -170,3 +170,21 @@ def test_new_outputs_on_another_stream(path, kind):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert sfa.sfa_check_device_status(c.h) == sfa.SFA_OK
+
+
+@pytest.mark.skipif(sfa._fast is None, reason="the extension is not built")
+def test_calls_without_outputs_go_through_the_extension(monkeypatch):
+    c = _case(ctx=(300, 20))
+
+    def never(*args):
+        raise AssertionError("the ctypes path was taken")
+
+    for name in ("_append_fn", "_attend_fn", "_accept_fn"):
+        monkeypatch.setattr(c.cache, name, never)
+    monkeypatch.setattr(sfa, "_call_on", never)
+    pos, mask = sfa.sfa_tree_plan(c.h, ints([[-1, 0], [-1, -1]]), c.ctx_d)
+    qr, kr = c.cache.append(0, c.q, c.k, c.v, c.ctx_d, positions=pos, rope=sfa.SfaRope(), k_out=torch.empty_like(c.k))
+    out = c.cache.attend(0, qr, c.ctx_d, mask=mask)
+    c.cache.accept(0, 1, ints([[1, 0], [0, 1]]), ints([1, 2]), c.ctx_d)
+    assert sfa.sfa_check_device_status(c.h) == sfa.SFA_OK
+    assert out.shape == (1, 2, 2, c.h.cfg.hidden) and bool(torch.isfinite(out).all())
