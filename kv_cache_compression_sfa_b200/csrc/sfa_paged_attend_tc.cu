@@ -20,8 +20,9 @@
 // P overwrites the scores that it came from.  A product with q in shared memory
 // costs about as much for 64 keys as for 128 (it reads all of q), so PAIR, bound
 // by the tensor cores and the softmax together, loses by half steps what it gains
-// in overlap: 172 against 160 us (37 sequences of 8,192 tokens, 36 new ones
-// each); 64 keys of a row per thread with two threads a row took 260 us.
+// in overlap: 221 against 201 us (37 sequences of 8,192 tokens, 36 new ones
+// each); 64 keys of a row per thread with two threads a row took 260 us where the
+// present form, then with P in one part, took 160.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -181,10 +182,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // rest is at most 2^-7 of a weight and rounded, so that both together are within
 // 2^-15 of it.  Neither is negative, and the rest is above zero wherever P is: an
 // infinite value that a row sees stays one in the sum of its products.
-// Measured with two parts and with one: 256 sequences of 1,024 to 4,096
-// tokens 239 and 210 us, a tree of 64 over 65,500 tokens 111 and 88, chunks of
-// 2,048 tokens 243 and 187, one token over 1,024 11.0 and 10.9; errors against 64
-// bits (2-norm) 1.7e-3, which is the result's rounding, and 2.1 to 2.3e-3.
+// Measured for a second with two parts and with one: 256 sequences of 1,024 to 4,096
+// tokens 231 and 209 us, a tree of 64 over 65,500 tokens 109 and 88, chunks of
+// 2,048 tokens 236 and 186; errors against 64 bits (2-norm) 1.7e-3, which is the
+// result's rounding, and 2.1 to 2.3e-3.
 template <int N>
 __device__ __forceinline__ float store_probs(float* x, float scale, float base, uint32_t taddr) {
   const float2 sc = make_float2(scale, scale), nb = make_float2(-base, -base);
@@ -338,8 +339,8 @@ attend_tc_kernel(const __grid_constant__ AttendParams p, const __grid_constant__
   if (warp == kTcMmaWarp) tmem_alloc(&sh.tmem, kTmemCols);
   // Rows of q that no copy writes stay zero: their products cost the tensor
   // cores less power, which sets the clock of a card that streams a cache
-  // (256 sequences of one token for a second: 220 us, and 237 with whatever lay
-  // there; with products of 64 rows about 200).
+  // (256 sequences of one token for a second: 231 us, 240 with whatever lay there,
+  // and 254 with products of 128 rows).
   for (int i = tid; i < (PAIR ? 2 : 1) * P::tile / 16; i += kTcThreads)
     reinterpret_cast<uint4*>(smem + P::q)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
