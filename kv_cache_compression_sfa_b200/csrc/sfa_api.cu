@@ -8,6 +8,8 @@
 //        defaults, engine init(n_layers, hidden) / per-layer enhancement call.
 //   [P3] "Dalin Soma SFA基于信号场注意力机制的神经网络推理加速框架" §2.2:
 //        alpha_layer = alpha_base·(0.3 + 0.7·layer_ratio)·decay^layer.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -178,12 +180,23 @@ bool handle_ok(const sfa_handle* h) { return h != nullptr && h->magic == kHandle
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA; }
 
-// Makes the current device's context current to this host thread: the driver
-// refuses to encode tensor maps in a thread that has made no CUDA call yet (the
-// runtime's own calls see to it themselves).
-cudaError_t bind_context(int* device) {
-  const cudaError_t e = cudaGetDevice(device);
-  return e == cudaSuccess ? cudaSetDevice(*device) : e;
+// Makes the current device's context current to this host thread if none is: the
+// driver refuses to encode tensor maps in a thread that has made no CUDA call yet
+// (the runtime's own calls see to it themselves).  A context that the caller has
+// made current stays.
+cudaError_t bind_context() {
+  static const PFN_cuCtxGetCurrent_v4000 current = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPoint("cuCtxGetCurrent", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(ptr) : nullptr;
+  }();
+  CUcontext ctx = nullptr;
+  if (current && current(&ctx) == CUDA_SUCCESS && ctx) return cudaSuccess;
+  int dev;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e == cudaSuccess ? cudaSetDevice(dev) : e;
 }
 
 // Near-field plan of the prefill: on the tensor cores where they apply (bf16
@@ -616,8 +629,7 @@ int prefill_impl(const sfa_handle* h, int layer_begin, int layer_count, const vo
   p.near = np;
   p.pool_smem = prefill_pool_smem();
   p.out_smem = prefill_out_smem();
-  int dev;
-  if (bind_context(&dev) != cudaSuccess) return SFA_ERR_CUDA;
+  if (bind_context() != cudaSuccess) return SFA_ERR_CUDA;
   return cuda_status(launch_prefill(p, c->in_dtype, c->head_dim, s));
 }
 
@@ -670,8 +682,7 @@ int sfa_decode_step_ex(const sfa_handle* h, int layer_begin, int layer_count, co
   const bool tile = h->tile_ok && static_cast<long long>(layer_count) * n_seq <= 0x7fffffffLL &&
                     h->out_mode == SFA_OUT_F32 &&
                     (h->tile_mode == 1 || (h->tile_mode < 0 && n_seq >= kDecodeTileMinSeqs));
-  int dev;
-  if (tile && bind_context(&dev) != cudaSuccess) return SFA_ERR_CUDA;
+  if (tile && bind_context() != cudaSuccess) return SFA_ERR_CUDA;
   if (tile) return cuda_status(launch_decode_tile(p, c->in_dtype, c->head_dim, s));
   return cuda_status(launch_decode(p, c->in_dtype, c->head_dim, s));
 }
@@ -831,8 +842,7 @@ int sfa_kv_attend(const sfa_handle* h, const sfa_kv_cache* cache, int layer_begi
   if (tiles > 1073741824.0) return SFA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < a.total) return SFA_ERR_WORKSPACE;
   if (!on_device(h)) return SFA_ERR_INVALID_ARG;
-  int dev;
-  if (c->in_dtype == SFA_BF16 && bind_context(&dev) != cudaSuccess) return SFA_ERR_CUDA;
+  if (c->in_dtype == SFA_BF16 && bind_context() != cudaSuccess) return SFA_ERR_CUDA;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   p.q = q;
   p.out = out;
