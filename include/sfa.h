@@ -418,8 +418,8 @@ typedef struct sfa_rope {
  * ctx_lens[b] + depth of the node (0 for a node without parent); mask
  * [batch][n_max][(n_max + 31) / 32]: bit j % 32 of word j / 32 of row i is 1
  * where node j is node i or one of its ancestors.  Either output may be NULL.
- * A sequence with a parent out of range is skipped and latched as
- * SFA_ERR_INVALID_ARG.  SFA_ERR_UNSUPPORTED for n_max > SFA_TREE_MAX. */
+ * A sequence with a parent out of range, or with ctx_lens + lens past 2^31 - 1,
+ * is skipped and latched as SFA_ERR_INVALID_ARG.  SFA_ERR_UNSUPPORTED for n_max > SFA_TREE_MAX. */
 SFA_API int sfa_tree_plan(const sfa_handle* h, const int* parents, int n_max, const int* lens,
                           const int* ctx_lens, int batch, int* positions, uint32_t* mask, void* stream);
 

@@ -25,7 +25,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(PlanParams p) {
   const int b = blockIdx.x;
   const int ctx = p.ctx[b];
   const int len = p.lens ? p.lens[b] : p.n_max;
-  bool ok = ctx >= 0 && len >= 0 && len <= p.n_max;
+  bool ok = ctx >= 0 && len >= 0 && len <= p.n_max && ctx <= 0x7fffffff - len;  // positions fit 32 bits
   if (ok)
     for (int i = threadIdx.x; i < len; i += kPlanThreads) {
       const int q = p.parents[static_cast<long long>(b) * p.n_max + i];
