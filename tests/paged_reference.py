@@ -10,8 +10,9 @@ visible keys of which the row's largest probability is p <= 1:
     (2u: the tensor cores may truncate where they add);
   * the exponential and the running rescale add 2^-21 relative, and sums of N
     terms N 2u; all of these enter numerator and denominator, hence twice;
-  * with bf16 inputs each p is rounded to bf16 before it meets v (2^-8), and
-    again enters numerator and denominator;
+  * with bf16 inputs each p may be rounded to bf16 before it meets v (2^-8), and
+    again enters numerator and denominator (the kernel's p is two bf16 numbers:
+    paged_bound has that narrower bound);
   * the result is rounded once: h |o|.
 append: the angle's fraction of a turn is held to 2^-25, which is 2^-22 of
 arc; sine, cosine and two products add as much: 2^-20 (|x1| + |x2|), and the
