@@ -528,23 +528,26 @@ class SfaOperator:
                            rows * cfg.hidden)
         self._in_dtype = cfg.torch_dtype
         self._decode_fn = load_library().sfa_decode_step
-        self.workspace, self._in_graph, self._kept = None, False, []
+        self.workspace, self._workspace_on, self._in_graph, self._kept = None, None, False, []
         if max_prefill > 0:
             self._ensure_workspace(max_prefill)
         self.reset()
 
     def _grow_workspace(self, need: int, stream=None):
         """A workspace of at least `need` bytes; one serves all calls, which the
-        operator's state puts in order.  The buffer that a larger one replaces may
-        still be in use by work enqueued on `stream`, and goes back behind it; one
-        that a graph has captured is kept as long as the operator."""
+        operator's state puts in order.  It is marked as used on every stream but
+        the one whose pool it came from, so that a buffer that a larger one replaces
+        goes back behind all calls; one that a graph has captured is kept as long as
+        the operator."""
+        on = _stream_ptr(stream)
         if self.workspace is None or self.workspace.numel() < need:
-            if self.workspace is not None:
-                if self._in_graph:
-                    self._kept.append(self.workspace)
-                elif stream is not None:
-                    self.workspace.record_stream(_stream_object(stream, self.device))
+            if self._in_graph:
+                self._kept.append(self.workspace)
             self.workspace, self._in_graph = _empty_on(stream, need, self.device), False
+            self._workspace_on = on
+        elif on != self._workspace_on:
+            self.workspace.record_stream(torch.cuda.current_stream(self.device) if stream is None
+                                         else _stream_object(stream, self.device))
         self._in_graph = self._in_graph or _capturing(stream, self.device)
 
     def _ensure_workspace(self, n: int, stream=None):

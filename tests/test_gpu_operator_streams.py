@@ -70,3 +70,24 @@ def test_new_outputs_and_workspace_on_another_stream(kind):
         live = ~torch.isnan(want[0])
         assert torch.equal(torch.isnan(got[0]), ~live) and torch.equal(got[0][live], want[0][live])
         assert torch.equal(got[1], want[1])
+
+
+def test_calls_on_several_streams_in_order():
+    """One operator on three streams that wait for one another, its workspace
+    growing between them."""
+    w, slots, src = _setup()
+    parts = [src.get(0, 70), src.get(70, 400), src.get(400, 420), src.get(420, 1200)]
+    ref = sfa.SfaOperator(sfa_config(w), slots, w.batch, max_prefill=800, device="cuda")
+    want = [ref.prefill(*x) for x in parts]
+    op = sfa.SfaOperator(sfa_config(w), slots, w.batch, device="cuda")
+    streams = [torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.current_stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got, before = [], None
+    for x, s in zip(parts, streams):
+        if before is not None:
+            s.wait_stream(before)
+        got.append(op.prefill(*x, stream=None if s is torch.cuda.current_stream() else s))
+        before = s
+    torch.cuda.synchronize()
+    assert op.check() == sfa.SFA_OK
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -89,3 +89,17 @@ def test_a_ragged_outputs_fill_comes_before_the_wait(op, log, monkeypatch):  # n
     out = op.prefill_ragged(*_inputs(4), torch.zeros(3, dtype=torch.int32), stream=0x200)
     names = [e[:2] for e in log]
     assert names.index(("fill", out.data_ptr())) < names.index(("wait", 0x200))
+
+
+def test_a_workspace_is_marked_as_used_on_every_other_stream(op, log):  # noqa: F811
+    """Whatever stream its calls ran on, it goes back behind all of them."""
+    op.prefill(*_inputs(8), stream=0x200)
+    ptr = op.workspace.data_ptr()
+    log.clear()
+    op.prefill(*_inputs(8), stream=0x200)
+    assert ("used on", ptr, 0x200) not in log    # the pool that it came from
+    op.prefill(*_inputs(4), stream=FakeStream(0x300))
+    op.prefill(*_inputs(4))
+    op.prefill_layers(0, *_inputs(64), stream=0x200)
+    assert op.workspace.data_ptr() != ptr
+    assert ("used on", ptr, 0x300) in log and ("used on", ptr, CURRENT) in log
